@@ -511,6 +511,178 @@ int dg_k_grouped_fp8_gemm_tn_contiguous(const uint8_t *A, const float *sfa,
 
 int dg_get_device_status(dg_stream_t stream, int *status);
 
+/* ------------------------------------------------------------------ MXFP4
+ *
+ * 4-bit microscaled operands (OCP Microscaling Formats specification 1.0,
+ * MXFP4): E2M1 elements (0, 0.5, 1, 1.5, 2, 3, 4, 6 and their negatives), one
+ * UE8M0 scale 2^(e - 127) per 32 consecutive K elements of a row; e = 255 is
+ * NaN.
+ *
+ *   codes   uint8 [rows][K/2]: element 2i of a row in the low nibble of byte
+ *           i, element 2i + 1 in the high one.
+ *   scales  int32 [ceil(rows/128)][ceil(K/128)][32][4]: word (b, p, r, c)
+ *           holds K groups 4p .. 4p+3 of row 128 b + 32 c + r, group 4p + t in
+ *           bits 8t .. 8t+7 (packed UE8M0 words as dg_pack_ue8m0's, in
+ *           512-byte blocks of 128 rows as the tensor cores read them).
+ *           Groups past K are zero bytes; the words of rows past `rows` are
+ *           never used (dg_quantize_mxfp4 writes zeros).
+ *   A batch (or the experts' weights) is one such tensor after the other.
+ */
+
+/*
+ * dg_quantize_mxfp4 -- quantizes the rows of x, or its columns.
+ *
+ * Per group of 32: amax = max |x|, scale = the smallest 2^e >= 2^-127 with
+ * 6 * 2^e >= amax (the rule of DG_SCALE_POW2: no element saturates), codes
+ * E2M1_RNE(x / scale).  A value that rounds to zero keeps its sign.  A group of
+ * zeros has scale byte 0; a group that holds an infinity or a NaN has scale
+ * byte 255 (every element reads as NaN) and codes 0.
+ *
+ *   x          device float or BF16 (x_dtype).  transpose == 0: [batch][M][ld_x],
+ *              batch stride M * ld_x, ld_x >= K, base and row stride 16-byte
+ *              aligned.  transpose == 1: [K][ld_x], ld_x >= M, batch == 1, no
+ *              alignment beyond the element's: the operand is x's transpose
+ *              (row m is column m of x, groups run down the rows of x), as
+ *              the backward products need it.
+ *   q          device uint8 [batch][M][K/2].
+ *   sf         device int32 [batch][ceil(M/128)][ceil(K/128)][32][4], written
+ *              whole.
+ *   batch >= 1, M >= 0 (0 is a no-op), K > 0, K % 32 == 0, all < 2^31; q and
+ *   sf 16-byte aligned.  Deterministic.
+ */
+int dg_quantize_mxfp4(const void *x, int x_dtype, int64_t batch, int64_t M,
+                      int64_t K, int64_t ld_x, int transpose, uint8_t *q,
+                      int32_t *sf, dg_stream_t stream);
+
+/*
+ * dg_dequantize_mxfp4 -- the values of an MXFP4 operand.
+ *
+ *   q, sf   as dg_quantize_mxfp4 writes them.
+ *   y       device float or BF16 (y_dtype) [batch][M][ld_y], ld_y >= K (the
+ *           elements past K are left as they are); exact in both types,
+ *           scales that take a value out of the type's range aside.
+ *   Sizes as above; q, sf, y and y's row stride 16-byte aligned.
+ */
+int dg_dequantize_mxfp4(const uint8_t *q, const int32_t *sf, int64_t batch,
+                        int64_t M, int64_t K, void *y, int y_dtype,
+                        int64_t ld_y, dg_stream_t stream);
+
+/*
+ * dg_mxfp4_gemm_nt -- D = A * B^T of two MXFP4 operands, both K-major.
+ *
+ *   D[i][j] = sum over groups g of 2^(ea[i][g] + eb[j][g] - 254)
+ *             * sum_{k < 32} A[i][32 g + k] * B[j][32 g + k]
+ * accumulated in FP32, rounded once to BF16.
+ *
+ *   A, sfa  device codes [M][K/2] and scale words of A; B, sfb of B [N][K/2].
+ *   D       device BF16 [M][N].
+ *   M >= 0 (0 is a no-op), N > 0, N % 8 == 0, K > 0, K % 32 == 0; all
+ *   pointers 16-byte aligned.  Few rows: K is split over the CTAs of a
+ *   thread-block cluster, which join their sums in a fixed order; no
+ *   workspace.  Deterministic.
+ */
+int dg_mxfp4_gemm_nt(const uint8_t *A, const int32_t *sfa, const uint8_t *B,
+                     const int32_t *sfb, void *D, int64_t M, int64_t N,
+                     int64_t K, dg_stream_t stream);
+
+/*
+ * dg_m_grouped_mxfp4_gemm_nt_contiguous -- the contiguous m-grouped product of
+ * dg_m_grouped_fp8_gemm_nt_contiguous with MXFP4 operands.
+ *
+ *   A, sfa     device codes [M_total][K/2] and scale words; B, sfb the experts'
+ *              [G][N][K/2] and [G][ceil(N/128)][ceil(K/128)][32][4].
+ *   D          device BF16 [M_total][N]; padding rows are not written.
+ *   m_indices  device int32 [M_total]: the expert of each row, -1 = padding;
+ *              the non-negative entries of each 128-row block are one expert,
+ *              else DG_ERR_DEVICE_DATA is recorded and only the rows of the
+ *              block's first expert are computed (none, if that is >= G).
+ *   M_total % 128 == 0, G >= 1; N, K and alignment as in dg_mxfp4_gemm_nt.
+ */
+int dg_m_grouped_mxfp4_gemm_nt_contiguous(const uint8_t *A, const int32_t *sfa,
+                                          const uint8_t *B, const int32_t *sfb,
+                                          void *D, const int32_t *m_indices,
+                                          int64_t M_total, int64_t N, int64_t K,
+                                          int G, dg_stream_t stream);
+
+/*
+ * dg_m_grouped_mxfp4_gemm_nt_masked -- the masked m-grouped product of
+ * dg_m_grouped_fp8_gemm_nt_masked with MXFP4 operands.
+ *
+ *   A, sfa    device codes [G][M_max][K/2] and scale words
+ *             [G][ceil(M_max/128)][ceil(K/128)][32][4]; B, sfb the experts'.
+ *   D         device BF16 [G][M_max][N]; rows >= masked_m[g] are not written.
+ *   masked_m  device int32 [G], each in [0, M_max]; others are clamped and
+ *             recorded as DG_ERR_DEVICE_DATA.  Read on the device only: the
+ *             call can be captured into a graph and replayed with other counts.
+ *   1 <= G <= 1024, M_max >= 1; N, K and alignment as in dg_mxfp4_gemm_nt.
+ */
+int dg_m_grouped_mxfp4_gemm_nt_masked(const uint8_t *A, const int32_t *sfa,
+                                      const uint8_t *B, const int32_t *sfb,
+                                      void *D, const int32_t *masked_m, int G,
+                                      int64_t M_max, int64_t N, int64_t K,
+                                      dg_stream_t stream);
+
+/* ------------------------------------------------------------------ routing
+ *
+ * dg_moe_route -- which experts each token goes to, how many tokens each
+ * expert gets (masked_m of the masked GEMMs; the segment sizes of the
+ * contiguous ones), and the balance loss.
+ *
+ * Per token t that routes, p = softmax(logits[t]):
+ *   idx[t][j]      the top_k experts of the largest logits, in descending
+ *                  order, equal logits in ascending order of the expert;
+ *   weights[t][j]  p of that expert, divided by the sum over the chosen
+ *                  ones if `normalize`;
+ *   counts[e]      the number of (t, j) with idx[t][j] == e;
+ *   loss[0]        E / (top_k n^2) * sum_e counts[e] * sum_t p[t][e];
+ *   num_tokens[0]  n, the tokens that route.
+ * An expert whose logit is -inf is closed to the token: with fewer than top_k
+ * open experts the remaining choices are idx -1, weight 0.  A token does not
+ * route (all its choices -1 and 0) if token_mask[t] is 0, if every expert is
+ * closed to it, or if its row holds a NaN or +inf; the last is recorded as
+ * DG_ERR_DEVICE_DATA unless the mask leaves the token out.  n == 0 gives loss 0.
+ *
+ *   logits      device float or BF16 (dtype) [T][ld], ld >= E, < 2^31.
+ *   token_mask  device uint8 [T], or NULL (all tokens).
+ *   idx, weights  device int32 / float [T][top_k]; counts int32 [E]; loss
+ *               float [1]; num_tokens int32 [1].
+ *   workspace   device scratch of dg_moe_route_workspace_size(T, E) bytes,
+ *               16-byte aligned (NULL where that is 0); calls that overlap need
+ *               one each.
+ *   0 <= T < 2^31, 1 <= E <= 1024, 1 <= top_k <= min(E, 32), normalize 0 or 1.
+ *   Pointers aligned to their elements.  Deterministic for a given SM count.
+ */
+int dg_moe_route(const void *logits, int dtype, int64_t T, int E, int64_t ld,
+                 int top_k, int normalize, const uint8_t *token_mask,
+                 int32_t *idx, float *weights, int32_t *counts, float *loss,
+                 int32_t *num_tokens, void *workspace, size_t workspace_bytes,
+                 dg_stream_t stream);
+
+/* Scratch bytes of dg_moe_route on the current device. */
+size_t dg_moe_route_workspace_size(int64_t T, int E);
+
+/*
+ * dg_moe_route_backward -- the gradient of dg_moe_route's logits from those of
+ * its weights and of its loss (counts are constants):
+ *   c[e] = dloss[0] * E / (top_k n^2) * counts[e]
+ *   dlogits[t][e] = p[e] (c[e] - <p, c>)
+ *       + (normalize) w_j (dw_j - <w, dw>) where e = idx[t][j]
+ *       + (else)      w_j dw_j where e = idx[t][j], - p[e] <w, dw>
+ * Zero for tokens that did not route, for closed experts, and for the
+ * gradients of choices that are -1.
+ *
+ *   idx, weights, counts, num_tokens  as dg_moe_route wrote them.
+ *   dweights  device float [T][top_k], or NULL (zero); dloss device float [1],
+ *             or NULL (zero).
+ *   dlogits   device [T][E] of the logits' type.
+ */
+int dg_moe_route_backward(const void *logits, int dtype, int64_t T, int E,
+                          int64_t ld, int top_k, int normalize,
+                          const int32_t *idx, const float *weights,
+                          const int32_t *counts, const int32_t *num_tokens,
+                          const float *dweights, const float *dloss,
+                          void *dlogits, dg_stream_t stream);
+
 #ifdef __cplusplus
 }
 #endif

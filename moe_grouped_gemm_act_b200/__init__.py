@@ -29,6 +29,15 @@ Entry points (same names as the C ABI):
 * ``dg_fp8_gemm_nt_ue8m0(a, sfa, b, sfb, d)``, ``dg_m_grouped_fp8_gemm_nt_masked_ue8m0(
   a, sfa, b, sfb, d, masked_m)``  power-of-two scales as packed UE8M0 words,
   applied by the tensor cores
+* ``dg_quantize_mxfp4(x, transpose=False)`` -> (q, sf)  1 x 32 MXFP4 (E2M1 codes,
+  UE8M0 scale words) of the rows or the columns of x;
+  ``dg_dequantize_mxfp4(q, sf, dtype)`` reads them back
+* ``dg_mxfp4_gemm_nt(a, sfa, b, sfb, d)``,
+  ``dg_m_grouped_mxfp4_gemm_nt_contiguous(a, sfa, b, sfb, d, m_indices)``,
+  ``dg_m_grouped_mxfp4_gemm_nt_masked(a, sfa, b, sfb, d, masked_m)``
+* ``dg_moe_route(logits, top_k)`` -> (idx, weights, counts, loss, num_tokens)
+  softmax top-k routing with per-expert counts and the balance loss;
+  ``dg_moe_route_backward(...)`` -> dlogits
 * ``dg_get_device_status()``, helpers ``dg_get_tma_aligned_size``,
   ``dg_get_mk_alignment_for_contiguous_layout``, ``dg_set_num_sms``,
   ``dg_get_num_sms``, ``dg_fp8_gemm_nt_workspace_size``.
@@ -67,6 +76,9 @@ EXPORTS = [
     "dg_m_grouped_fp8_gemm_nt_contiguous",
     "dg_m_grouped_fp8_gemm_nt_masked", "dg_k_grouped_fp8_gemm_nt_contiguous",
     "dg_get_device_status",
+    "dg_quantize_mxfp4", "dg_dequantize_mxfp4", "dg_mxfp4_gemm_nt",
+    "dg_m_grouped_mxfp4_gemm_nt_contiguous", "dg_m_grouped_mxfp4_gemm_nt_masked",
+    "dg_moe_route", "dg_moe_route_workspace_size", "dg_moe_route_backward",
 ]
 
 _lib = None
@@ -119,6 +131,18 @@ def load_library(path: str = LIB_PATH) -> ctypes.CDLL:
         "dg_k_grouped_fp8_gemm_nt_contiguous":
             (I, [P, P, I64, P, P, I64, P, P, P, I, I64, I64, I64, P]),
         "dg_get_device_status": (I, [P, ctypes.POINTER(ctypes.c_int)]),
+        "dg_quantize_mxfp4": (I, [P, I, I64, I64, I64, I64, I, P, P, P]),
+        "dg_dequantize_mxfp4": (I, [P, P, I64, I64, I64, P, I, I64, P]),
+        "dg_mxfp4_gemm_nt": (I, [P, P, P, P, P, I64, I64, I64, P]),
+        "dg_m_grouped_mxfp4_gemm_nt_contiguous":
+            (I, [P, P, P, P, P, P, I64, I64, I64, I, P]),
+        "dg_m_grouped_mxfp4_gemm_nt_masked":
+            (I, [P, P, P, P, P, P, I, I64, I64, I64, P]),
+        "dg_moe_route":
+            (I, [P, I, I64, I, I64, I, I, P, P, P, P, P, P, P, SZ, P]),
+        "dg_moe_route_workspace_size": (SZ, [I64, I]),
+        "dg_moe_route_backward":
+            (I, [P, I, I64, I, I64, I, I, P, P, P, P, P, P, P, P]),
     }
     for name, (res, args) in sig.items():
         fn = getattr(lib, name)
@@ -626,3 +650,266 @@ def dg_m_grouped_fp8_gemm_nt_masked_ue8m0(a, sfa, b, sfb, d, masked_m,
         _ptr(masked_m), g, m_max, n, k, _stream(stream))
     _check(rc, "dg_m_grouped_fp8_gemm_nt_masked_ue8m0")
     return d
+
+
+# ------------------------------------------------------------------ MXFP4, routing
+_DTYPES = {torch.float32: DG_DTYPE_F32, torch.bfloat16: DG_DTYPE_BF16}
+
+
+def _on_device(name, fn_args, *ts, stream=None):
+    """Calls entry point `name` with fn_args and the stream, on the device that
+    the tensors ts (None allowed) share: their own current stream if none is
+    given, whatever device is current."""
+    dev = None
+    for t in ts:
+        if t is None:
+            continue
+        if not t.is_cuda:
+            raise ValueError("all tensors must be CUDA tensors (there is no CPU path)")
+        if dev is None:
+            dev = t.device
+        elif t.device != dev:
+            raise ValueError(f"tensors on {dev} and {t.device}: all must be on one device")
+    if stream is None:
+        stream = torch.cuda.current_stream(dev)
+    elif stream.device != dev:
+        raise ValueError(f"the stream is on {stream.device}, the tensors on {dev}")
+    fn = getattr(load_library(), name)
+    if torch.cuda.current_device() == dev.index:
+        rc = fn(*fn_args, stream.cuda_stream)
+    else:
+        with torch.cuda.device(dev):
+            rc = fn(*fn_args, stream.cuda_stream)
+    _check(rc, name)
+
+
+def _empty(shape, dtype, device, stream):
+    """An uninitialised tensor for a call on `stream`: it comes from that stream's
+    memory pool, so that nothing still running on the current stream holds it, and
+    is marked as used on the current stream, where the caller gets it."""
+    if stream is None:
+        return torch.empty(shape, dtype=dtype, device=device)
+    with torch.cuda.stream(stream):
+        t = torch.empty(shape, dtype=dtype, device=device)
+    t.record_stream(torch.cuda.current_stream(t.device))
+    return t
+
+
+def _contiguous(*ts):
+    for t in ts:
+        if t is not None and not t.is_contiguous():
+            raise ValueError("tensors must be contiguous")
+
+
+def _rows_2d(x, name):
+    """The row stride of a matrix whose rows are contiguous."""
+    if x.shape[1] > 1 and x.stride(1) != 1:
+        raise ValueError(f"{name}: the elements of a row must be contiguous")
+    ld = x.stride(0) if x.shape[0] > 1 else x.shape[1]
+    if ld < x.shape[1]:
+        raise ValueError(f"{name}: rows overlap (row stride {ld} of {x.shape[1]} elements)")
+    return ld
+
+
+def _mx_scales(rows, k):
+    """The shape of an operand's MXFP4 scale words."""
+    return (-(-rows // 128), -(-k // 128), 32, 4)
+
+
+def dg_quantize_mxfp4(x: torch.Tensor, transpose: bool = False, q=None, sf=None, stream=None):
+    """MXFP4 quantization (one UE8M0 scale per 32 K elements) of x [M, K] or
+    [B, M, K] (float32 or bfloat16), or, with ``transpose``, of the transpose of
+    x [K, M].  A 2-D x may have any row stride.
+
+    Returns (q uint8 [.., M, K/2], sf int32 [.., ceil(M/128), ceil(K/128), 32, 4]),
+    the layouts of include/dg.h."""
+    if x.dtype not in _DTYPES:
+        raise ValueError("x must be float32 or bfloat16")
+    if x.dim() not in (2, 3) or (transpose and x.dim() == 3):
+        raise ValueError(f"x must be a matrix (or a batch of them, not transposed), got shape "
+                         f"{tuple(x.shape)}")
+    if x.dim() == 3:
+        _contiguous(x)
+        lead, (m, k), ld = (x.shape[0],), x.shape[1:], x.shape[2]
+    else:
+        lead, ld = (), _rows_2d(x, "x")
+        m, k = (x.shape[1], x.shape[0]) if transpose else x.shape
+    if k <= 0 or k % 32:
+        raise ValueError(f"K = {k} must be a positive multiple of 32")
+    if lead == (0,):
+        raise ValueError("an empty batch")
+    if q is None:
+        q = _empty(lead + (m, k // 2), torch.uint8, x.device, stream)
+    if sf is None:
+        sf = _empty(lead + _mx_scales(m, k), torch.int32, x.device, stream)
+    _contiguous(q, sf)
+    _expect(q, "q", torch.uint8, lead + (m, k // 2))
+    _expect(sf, "sf", torch.int32, lead + _mx_scales(m, k))
+    _on_device("dg_quantize_mxfp4",
+               (_ptr(x), _DTYPES[x.dtype], lead[0] if lead else 1, m, k, ld, int(transpose),
+                _ptr(q), _ptr(sf)), x, q, sf, stream=stream)
+    return q, sf
+
+
+def dg_dequantize_mxfp4(q: torch.Tensor, sf: torch.Tensor, dtype: torch.dtype = torch.bfloat16,
+                        out=None, stream=None) -> torch.Tensor:
+    """The values of an MXFP4 operand (q [.., M, K/2], sf as dg_quantize_mxfp4
+    returns them) in bfloat16 or float32, both exact: [.., M, K]."""
+    if out is not None:
+        dtype = out.dtype
+    if dtype not in _DTYPES:
+        raise ValueError("dtype must be float32 or bfloat16")
+    if q.dim() not in (2, 3):
+        raise ValueError(f"q must be [M, K/2] or [B, M, K/2], got shape {tuple(q.shape)}")
+    lead, (m, kh) = tuple(q.shape[:-2]), q.shape[-2:]
+    k = 2 * kh
+    if k <= 0 or k % 32:
+        raise ValueError(f"K = {k} must be a positive multiple of 32")
+    if lead == (0,):
+        raise ValueError("an empty batch")
+    if out is None:
+        out = _empty(lead + (m, k), dtype, q.device, stream)
+    _contiguous(q, sf, out)
+    _expect(q, "q", torch.uint8, lead + (m, kh))
+    _expect(sf, "sf", torch.int32, lead + _mx_scales(m, k))
+    _expect(out, "out", dtype, lead + (m, k))
+    _on_device("dg_dequantize_mxfp4",
+               (_ptr(q), _ptr(sf), lead[0] if lead else 1, m, k, _ptr(out), _DTYPES[dtype], k),
+               q, sf, out, stream=stream)
+    return out
+
+
+def _mx_operands(a, sfa, b, sfb, d, m, n, k, lead_a, lead_b):
+    _contiguous(a, sfa, b, sfb, d)
+    _expect(a, "a", torch.uint8, lead_a + (m, k // 2))
+    _expect(sfa, "sfa", torch.int32, lead_a + _mx_scales(m, k))
+    _expect(b, "b", torch.uint8, lead_b + (n, k // 2))
+    _expect(sfb, "sfb", torch.int32, lead_b + _mx_scales(n, k))
+    _expect(d, "d", torch.bfloat16, lead_a + (m, n))
+
+
+def dg_mxfp4_gemm_nt(a, sfa, b, sfb, d, stream=None) -> torch.Tensor:
+    """D = A * B^T of two MXFP4 operands: a [M, K/2] and b [N, K/2] uint8 with
+    their scale words (dg_quantize_mxfp4), N % 8 == 0; d a preallocated bfloat16
+    [M, N] tensor, returned."""
+    if a.dim() != 2 or b.dim() != 2:
+        raise ValueError("a and b must be [M, K/2] and [N, K/2]")
+    m, k, n = a.shape[0], 2 * a.shape[1], b.shape[0]
+    _mx_operands(a, sfa, b, sfb, d, m, n, k, (), ())
+    _on_device("dg_mxfp4_gemm_nt",
+               (_ptr(a), _ptr(sfa), _ptr(b), _ptr(sfb), _ptr(d), m, n, k),
+               a, sfa, b, sfb, d, stream=stream)
+    return d
+
+
+def dg_m_grouped_mxfp4_gemm_nt_contiguous(a, sfa, b, sfb, d, m_indices,
+                                          stream=None) -> torch.Tensor:
+    """Contiguous m-grouped product of MXFP4 operands: a [M_total, K/2], b [G, N,
+    K/2], m_indices int32 [M_total] (-1 = padding); padding rows of d are not
+    written."""
+    if a.dim() != 2 or b.dim() != 3:
+        raise ValueError("a and b must be [M_total, K/2] and [G, N, K/2]")
+    m, k = a.shape[0], 2 * a.shape[1]
+    g, n = b.shape[:2]
+    _mx_operands(a, sfa, b, sfb, d, m, n, k, (), (g,))
+    _contiguous(m_indices)
+    _expect(m_indices, "m_indices", torch.int32, (m,))
+    _on_device("dg_m_grouped_mxfp4_gemm_nt_contiguous",
+               (_ptr(a), _ptr(sfa), _ptr(b), _ptr(sfb), _ptr(d), _ptr(m_indices), m, n, k, g),
+               a, sfa, b, sfb, d, m_indices, stream=stream)
+    return d
+
+
+def dg_m_grouped_mxfp4_gemm_nt_masked(a, sfa, b, sfb, d, masked_m, stream=None) -> torch.Tensor:
+    """Masked m-grouped product of MXFP4 operands: a [G, M_max, K/2], b [G, N,
+    K/2], masked_m int32 [G] on the device (dg_moe_route's counts); rows >=
+    masked_m[g] of d are not written."""
+    if a.dim() != 3 or b.dim() != 3:
+        raise ValueError("a and b must be [G, M_max, K/2] and [G, N, K/2]")
+    g, m, k = a.shape[0], a.shape[1], 2 * a.shape[2]
+    n = b.shape[1]
+    _mx_operands(a, sfa, b, sfb, d, m, n, k, (g,), (g,))
+    _contiguous(masked_m)
+    _expect(masked_m, "masked_m", torch.int32, (g,))
+    _on_device("dg_m_grouped_mxfp4_gemm_nt_masked",
+               (_ptr(a), _ptr(sfa), _ptr(b), _ptr(sfb), _ptr(d), _ptr(masked_m), g, m, n, k),
+               a, sfa, b, sfb, d, masked_m, stream=stream)
+    return d
+
+
+def dg_moe_route_workspace_size(t: int, e: int) -> int:
+    return load_library().dg_moe_route_workspace_size(t, e)
+
+
+def _route_logits(logits):
+    if logits.dtype not in _DTYPES:
+        raise ValueError("logits must be float32 or bfloat16")
+    if logits.dim() != 2:
+        raise ValueError(f"logits must be [T, E], got shape {tuple(logits.shape)}")
+    return logits.shape[0], logits.shape[1], _rows_2d(logits, "logits")
+
+
+def dg_moe_route(logits: torch.Tensor, top_k: int, normalize: bool = True, token_mask=None,
+                 stream=None):
+    """Softmax top-k routing of logits [T, E] (float32 or bfloat16, any row
+    stride) with the per-expert counts and the balance loss (include/dg.h).
+    token_mask: bool or uint8 [T], False for tokens that do not route.
+
+    Returns (idx int32 [T, top_k], weights float32 [T, top_k], counts int32 [E],
+    loss float32 [1], num_tokens int32 [1]); -1 / 0 where a token has no choice."""
+    t, e, ld = _route_logits(logits)
+    dev = logits.device
+    if token_mask is not None:
+        _contiguous(token_mask)
+        if token_mask.dtype not in (torch.bool, torch.uint8):
+            raise ValueError("token_mask must be bool or uint8")
+        _expect(token_mask, "token_mask", token_mask.dtype, (t,))
+    if not 1 <= top_k <= min(e, 32):
+        raise ValueError(f"top_k = {top_k} must be in 1 .. min(E, 32), E = {e}")
+    if not logits.is_cuda:
+        raise ValueError("all tensors must be CUDA tensors (there is no CPU path)")
+    idx = _empty((t, top_k), torch.int32, dev, stream)
+    weights = _empty((t, top_k), torch.float32, dev, stream)
+    counts = _empty((e,), torch.int32, dev, stream)
+    loss = _empty((1,), torch.float32, dev, stream)
+    num_tokens = _empty((1,), torch.int32, dev, stream)
+    if torch.cuda.current_device() == dev.index:
+        nbytes = dg_moe_route_workspace_size(t, e)
+    else:
+        with torch.cuda.device(dev):
+            nbytes = dg_moe_route_workspace_size(t, e)
+    ws = _empty((nbytes,), torch.uint8, dev, stream) if nbytes else None
+    _on_device("dg_moe_route",
+               (_ptr(logits), _DTYPES[logits.dtype], t, e, ld, top_k, int(bool(normalize)),
+                _ptr(token_mask), _ptr(idx), _ptr(weights), _ptr(counts), _ptr(loss),
+                _ptr(num_tokens), _ptr(ws), nbytes), logits, token_mask, stream=stream)
+    return idx, weights, counts, loss, num_tokens
+
+
+def dg_moe_route_backward(logits, idx, weights, counts, num_tokens, dweights=None, dloss=None,
+                          normalize: bool = True, stream=None) -> torch.Tensor:
+    """The gradient of dg_moe_route's logits, in their type: from dweights
+    (float32 [T, top_k]) and dloss (float32, one element), either None for zero;
+    idx, weights, counts and num_tokens as dg_moe_route returned them."""
+    t, e, ld = _route_logits(logits)
+    if idx.dim() != 2:
+        raise ValueError(f"idx must be [T, top_k], got shape {tuple(idx.shape)}")
+    k = idx.shape[1]
+    _contiguous(idx, weights, counts, num_tokens, dweights, dloss)
+    _expect(idx, "idx", torch.int32, (t, k))
+    _expect(weights, "weights", torch.float32, (t, k))
+    _expect(counts, "counts", torch.int32, (e,))
+    _expect(num_tokens, "num_tokens", torch.int32, (1,))
+    if dweights is not None:
+        _expect(dweights, "dweights", torch.float32, (t, k))
+    if dloss is not None:
+        if dloss.numel() != 1:
+            raise ValueError("dloss must have one element")
+        _expect(dloss, "dloss", torch.float32, tuple(dloss.shape))
+    dlogits = _empty((t, e), logits.dtype, logits.device, stream)
+    _on_device("dg_moe_route_backward",
+               (_ptr(logits), _DTYPES[logits.dtype], t, e, ld, k, int(bool(normalize)), _ptr(idx),
+                _ptr(weights), _ptr(counts), _ptr(num_tokens), _ptr(dweights), _ptr(dloss),
+                _ptr(dlogits)), logits, idx, weights, counts, num_tokens, dweights, dloss,
+               stream=stream)
+    return dlogits

@@ -1,0 +1,628 @@
+// moe_route.cu -- routing of tokens to experts: softmax, top-k, per-expert
+// counts and the balance loss, and the gradient of the logits.
+//
+// With p_t = softmax(logits_t) over the E experts and idx_t the k largest
+// logits of a token (ties go to the lowest index):
+//     w_tj     = p_t[idx_tj]            (normalized: divided by their sum)
+//     counts_e = #{(t, j): idx_tj = e}
+//     loss     = E / (k n^2) * sum_e counts_e * sum_t p_te
+// where n counts the tokens that route at all.  The loss is E times the inner
+// product of the experts' share of the choices and their mean probability;
+// the counts are constants in its gradient.
+//
+// Gradient, c_e = dloss * E / (k n^2) * counts_e, <.,.> over a token's experts:
+//     dlogits_e = p_e (c_e - <p, c>)
+//               + [e = idx_j]  w_j (dw_j - <w, dw>)     (normalized)
+//               + [e = idx_j]  w_j dw_j - p_e <w, dw>   (else)
+//
+// A warp takes a token, lane l the experts l V .. l V + V - 1 in registers, so
+// that a token is read once, in contiguous 16-byte loads where its row allows
+// them.  The top-k are k rounds of a warp maximum over order-preserving integer
+// keys; the lowest lane that holds the maximum has the lowest index.  Sums over
+// tokens are exact (counts) or taken in a fixed order (probabilities: per lane
+// over a warp's tokens, over the warps of a block, over the blocks), so a
+// repeated call gives the same bits.
+#include <cuda_bf16.h>
+#include <cuda_runtime.h>
+
+#include <cfloat>
+#include <cstdint>
+
+#include "dg.h"
+#include "internal.h"
+#include "ptx.cuh"
+
+namespace dg {
+
+namespace {
+
+constexpr int kWarps = 16;
+constexpr int kThreads = kWarps * 32;
+constexpr int kMaxExperts = 1024;
+constexpr int kMaxTopK = 32;  // lane j keeps choice j
+// Up to this many tokens one block does everything (one launch); above it a
+// second kernel joins the blocks' sums.
+constexpr int kSingleBlockTokens = 4 * kWarps;
+constexpr int kMaxBlocks = 148;
+
+// Order-preserving key of an FP32 value that is not NaN; -0 and +0 are one key.
+__device__ __forceinline__ uint32_t order_key(float x) {
+  const uint32_t u = __float_as_uint(x + 0.0f);
+  return (u & 0x80000000u) ? ~u : (u | 0x80000000u);
+}
+__device__ __forceinline__ float key_value(uint32_t k) {
+  return __uint_as_float((k & 0x80000000u) ? (k & 0x7FFFFFFFu) : ~k);
+}
+constexpr uint32_t kKeyNegInf = 0x007FFFFFu;  // order_key(-inf); 0: no candidate
+
+__device__ __forceinline__ float warp_sum(float v) {
+#pragma unroll
+  for (int o = 16; o > 0; o >>= 1) v += __shfl_xor_sync(0xffffffffu, v, o);
+  return v;
+}
+
+// Experts l V .. l V + V - 1 of a row of E logits, -inf past E.  `vec`: rows
+// start on a 16-byte boundary (or V elements, if that is less) and E % V == 0.
+template <int V>
+__device__ __forceinline__ void load_row(const float *row, int E, bool vec, float x[V]) {
+  const int e0 = (threadIdx.x & 31) * V;
+  if constexpr (V >= 2) {
+    if (vec) {
+      constexpr int S = V < 4 ? V : 4;
+#pragma unroll
+      for (int i = 0; i < V; i += S) {
+        if constexpr (S == 4) {
+          const float4 t = e0 < E ? __ldg(reinterpret_cast<const float4 *>(row + e0 + i))
+                                  : make_float4(-INFINITY, -INFINITY, -INFINITY, -INFINITY);
+          x[i] = t.x; x[i + 1] = t.y; x[i + 2] = t.z; x[i + 3] = t.w;
+        } else {
+          const float2 t = e0 < E ? __ldg(reinterpret_cast<const float2 *>(row + e0 + i))
+                                  : make_float2(-INFINITY, -INFINITY);
+          x[i] = t.x; x[i + 1] = t.y;
+        }
+      }
+      return;
+    }
+  }
+#pragma unroll
+  for (int i = 0; i < V; ++i) x[i] = e0 + i < E ? __ldg(row + e0 + i) : -INFINITY;
+}
+__device__ __forceinline__ void unpack_bf16(uint32_t w, float &a, float &b) {
+  a = __uint_as_float(w << 16);
+  b = __uint_as_float(w & 0xFFFF0000u);
+}
+template <int V>
+__device__ __forceinline__ void load_row(const __nv_bfloat16 *row, int E, bool vec, float x[V]) {
+  const int e0 = (threadIdx.x & 31) * V;
+  constexpr uint32_t kNegInf2 = 0xFF80FF80u;
+  if constexpr (V >= 2) {
+    if (vec) {
+      constexpr int S = V < 8 ? V : 8;
+#pragma unroll
+      for (int i = 0; i < V; i += S) {
+        if constexpr (S == 8) {
+          const uint4 t = e0 < E ? __ldg(reinterpret_cast<const uint4 *>(row + e0 + i))
+                                 : make_uint4(kNegInf2, kNegInf2, kNegInf2, kNegInf2);
+          unpack_bf16(t.x, x[i], x[i + 1]);
+          unpack_bf16(t.y, x[i + 2], x[i + 3]);
+          unpack_bf16(t.z, x[i + 4], x[i + 5]);
+          unpack_bf16(t.w, x[i + 6], x[i + 7]);
+        } else if constexpr (S == 4) {
+          const uint2 t = e0 < E ? __ldg(reinterpret_cast<const uint2 *>(row + e0 + i))
+                                 : make_uint2(kNegInf2, kNegInf2);
+          unpack_bf16(t.x, x[i], x[i + 1]);
+          unpack_bf16(t.y, x[i + 2], x[i + 3]);
+        } else {
+          const uint32_t t = e0 < E ? __ldg(reinterpret_cast<const uint32_t *>(row + e0 + i))
+                                    : kNegInf2;
+          unpack_bf16(t, x[i], x[i + 1]);
+        }
+      }
+      return;
+    }
+  }
+#pragma unroll
+  for (int i = 0; i < V; ++i)
+    x[i] = e0 + i < E
+               ? __uint_as_float(static_cast<uint32_t>(__ldg(
+                                     reinterpret_cast<const unsigned short *>(row) + e0 + i))
+                                 << 16)
+               : -INFINITY;
+}
+
+struct RouteParams {
+  const void *logits;
+  int64_t tokens, ld;
+  int experts, top_k, normalize, vec;
+  const uint8_t *mask;  // token routes when nonzero (nullptr: all do)
+  int32_t *idx;
+  float *weights;
+  int32_t *counts;
+  float *loss;
+  int32_t *num_tokens;
+  int32_t *part_counts;  // [blocks][E], then [blocks] routed tokens
+  float *part_psum;      // [blocks][E]
+  int *status;
+};
+
+// The sums of all blocks: counts, and the loss from the probabilities' sums.
+// `blocks` rows of E, each E consecutive; one block of kThreads threads.
+__device__ __forceinline__ void finish(const RouteParams &p, int blocks,
+                                       const int32_t *part_counts, const float *part_psum,
+                                       const int32_t *part_tokens, float *s_red) {
+  // each thread sums its experts over all blocks, in block order
+  float acc = 0.0f;
+  for (int e = threadIdx.x; e < p.experts; e += kThreads) {
+    int c = 0;
+    float s = 0.0f;
+#pragma unroll 8
+    for (int b = 0; b < blocks; ++b) {
+      c += part_counts[static_cast<int64_t>(b) * p.experts + e];
+      s += part_psum[static_cast<int64_t>(b) * p.experts + e];
+    }
+    p.counts[e] = c;
+    acc += static_cast<float>(c) * s;
+  }
+  int n = 0;
+  if (threadIdx.x < 32) {
+    for (int b = threadIdx.x; b < blocks; b += 32) n += part_tokens[b];
+    n = __reduce_add_sync(0xffffffffu, n);
+  }
+  acc = warp_sum(acc);
+  if ((threadIdx.x & 31) == 0) s_red[threadIdx.x >> 5] = acc;
+  __syncthreads();
+  if (threadIdx.x == 0) {
+    float total = 0.0f;
+    for (int w = 0; w < kWarps; ++w) total += s_red[w];
+    const float nf = static_cast<float>(n);
+    *p.loss = n > 0 ? total * (static_cast<float>(p.experts) /
+                               (static_cast<float>(p.top_k) * nf * nf))
+                    : 0.0f;
+    *p.num_tokens = n;
+  }
+}
+
+template <typename T, int V, bool SINGLE>
+__global__ void __launch_bounds__(kThreads)
+moe_route_kernel(const RouteParams p) {
+  extern __shared__ float s_mem[];  // [kWarps][E] probability sums, [E] counts
+  __shared__ float s_red[kWarps];
+  __shared__ int32_t s_tokens;
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const int E = p.experts, K = p.top_k;
+  float *s_psum = s_mem;
+  int32_t *s_counts = reinterpret_cast<int32_t *>(s_mem + kWarps * E);
+  grid_launch_dependents();
+  for (int e = threadIdx.x; e < E; e += kThreads) s_counts[e] = 0;
+  if (threadIdx.x == 0) s_tokens = 0;
+  __syncthreads();
+  grid_dependency_wait();
+
+  float psum[V];
+#pragma unroll
+  for (int i = 0; i < V; ++i) psum[i] = 0.0f;
+  int routed = 0;
+  const int64_t stride = static_cast<int64_t>(gridDim.x) * kWarps;
+  for (int64_t t = static_cast<int64_t>(blockIdx.x) * kWarps + warp; t < p.tokens; t += stride) {
+    float x[V];
+    load_row<V>(static_cast<const T *>(p.logits) + t * p.ld, E, p.vec != 0, x);
+    bool bad = false;
+    uint32_t key[V], top = 0;
+#pragma unroll
+    for (int i = 0; i < V; ++i) {
+      bad |= !(x[i] <= FLT_MAX);  // NaN or +inf
+      key[i] = order_key(x[i]);
+      if (lane * V + i >= E) key[i] = 0;
+      top = max(top, key[i]);
+    }
+    bad = __any_sync(0xffffffffu, bad);
+    const uint32_t first = __reduce_max_sync(0xffffffffu, top);
+    const bool masked = p.mask && !p.mask[t];
+    if (bad && !masked && lane == 0) record_status(p.status, DG_ERR_DEVICE_DATA);
+    int my_idx = -1;
+    float my_w = 0.0f;
+    if (!bad && !masked && first > kKeyNegInf) {
+      ++routed;
+      const float xmax = key_value(first);
+      float sum = 0.0f;
+#pragma unroll
+      for (int i = 0; i < V; ++i) {
+        x[i] = expf(x[i] - xmax);
+        sum += x[i];
+      }
+      const float inv = 1.0f / warp_sum(sum);
+#pragma unroll
+      for (int i = 0; i < V; ++i) psum[i] += x[i] * inv;
+      uint32_t best = first;
+      for (int j = 0; j < K; ++j) {
+        if (j) best = __reduce_max_sync(0xffffffffu, top);
+        if (best <= kKeyNegInf) break;  // only closed experts are left
+        const int owner = __ffs(__ballot_sync(0xffffffffu, top == best)) - 1;
+        int at = 0;
+        if (lane == owner) {
+          bool found = false;
+          top = 0;
+#pragma unroll
+          for (int i = 0; i < V; ++i) {
+            if (!found && key[i] == best) {
+              found = true;
+              at = lane * V + i;
+              key[i] = 0;
+            }
+            top = max(top, key[i]);
+          }
+        }
+        at = __shfl_sync(0xffffffffu, at, owner);
+        if (lane == j) {
+          my_idx = at;
+          my_w = expf(key_value(best) - xmax) * inv;
+        }
+      }
+      if (p.normalize) my_w /= warp_sum(my_w);
+      if (my_idx >= 0) atomicAdd(&s_counts[my_idx], 1);
+    }
+    if (lane < K) {
+      p.idx[t * K + lane] = my_idx;
+      p.weights[t * K + lane] = my_w;
+    }
+  }
+#pragma unroll
+  for (int i = 0; i < V; ++i)
+    if (lane * V + i < E) s_psum[warp * E + lane * V + i] = psum[i];
+  if (lane == 0) atomicAdd(&s_tokens, routed);
+  __syncthreads();
+  if constexpr (SINGLE) {
+    // the warps' sums first, into the first row
+    for (int e = threadIdx.x; e < E; e += kThreads) {
+      float s = 0.0f;
+#pragma unroll
+      for (int w = 0; w < kWarps; ++w) s += s_psum[w * E + e];
+      s_psum[e] = s;  // (only this thread reads column e)
+    }
+    finish(p, 1, s_counts, s_psum, &s_tokens, s_red);
+  } else {
+    for (int e = threadIdx.x; e < E; e += kThreads) {
+      float s = 0.0f;
+#pragma unroll
+      for (int w = 0; w < kWarps; ++w) s += s_psum[w * E + e];
+      p.part_psum[static_cast<int64_t>(blockIdx.x) * E + e] = s;
+      p.part_counts[static_cast<int64_t>(blockIdx.x) * E + e] = s_counts[e];
+    }
+    if (threadIdx.x == 0)
+      p.part_counts[static_cast<int64_t>(gridDim.x) * E + blockIdx.x] = s_tokens;
+  }
+}
+
+__global__ void __launch_bounds__(kThreads)
+moe_route_finish_kernel(const RouteParams p, int blocks) {
+  __shared__ float s_red[kWarps];
+  grid_launch_dependents();
+  grid_dependency_wait();
+  finish(p, blocks, p.part_counts, p.part_psum,
+         p.part_counts + static_cast<int64_t>(blocks) * p.experts, s_red);
+}
+
+// The gradient of the logits.  A token that did not route (idx[t][0] < 0) gets
+// zeros; its logits are not used, so what they hold does not matter.
+struct RouteBackwardParams {
+  const void *logits;
+  int64_t tokens, ld;
+  int experts, top_k, normalize, vec;
+  const int32_t *idx;
+  const float *weights;
+  const int32_t *counts;
+  const int32_t *num_tokens;
+  const float *dweights;  // nullptr: zero
+  const float *dloss;     // nullptr: zero
+  void *dlogits;          // [tokens][experts]
+};
+
+template <int V>
+__device__ __forceinline__ void store_row(float *row, int E, bool vec, const float g[V]) {
+  const int e0 = (threadIdx.x & 31) * V;
+  if constexpr (V >= 2) {
+    if (vec) {
+      if (e0 < E) {
+        constexpr int S = V < 4 ? V : 4;
+#pragma unroll
+        for (int i = 0; i < V; i += S) {
+          if constexpr (S == 4)
+            *reinterpret_cast<float4 *>(row + e0 + i) =
+                make_float4(g[i], g[i + 1], g[i + 2], g[i + 3]);
+          else
+            *reinterpret_cast<float2 *>(row + e0 + i) = make_float2(g[i], g[i + 1]);
+        }
+      }
+      return;
+    }
+  }
+#pragma unroll
+  for (int i = 0; i < V; ++i)
+    if (e0 + i < E) row[e0 + i] = g[i];
+}
+// BF16 gradients of BF16 logits: the one rounding, to nearest even.
+template <int V>
+__device__ __forceinline__ void store_row(__nv_bfloat16 *row, int E, bool vec, const float g[V]) {
+  const int e0 = (threadIdx.x & 31) * V;
+  if constexpr (V >= 2) {
+    if (vec) {
+      if (e0 < E) {
+        uint32_t w[V / 2];
+#pragma unroll
+        for (int i = 0; i < V / 2; ++i) {
+          const __nv_bfloat162 t = __floats2bfloat162_rn(g[2 * i], g[2 * i + 1]);
+          w[i] = *reinterpret_cast<const uint32_t *>(&t);
+        }
+        if constexpr (V >= 8) {
+#pragma unroll
+          for (int i = 0; i < V / 8; ++i)
+            reinterpret_cast<uint4 *>(row + e0)[i] =
+                make_uint4(w[4 * i], w[4 * i + 1], w[4 * i + 2], w[4 * i + 3]);
+        } else if constexpr (V == 4) {
+          *reinterpret_cast<uint2 *>(row + e0) = make_uint2(w[0], w[1]);
+        } else {
+          *reinterpret_cast<uint32_t *>(row + e0) = w[0];
+        }
+      }
+      return;
+    }
+  }
+#pragma unroll
+  for (int i = 0; i < V; ++i)
+    if (e0 + i < E) row[e0 + i] = __float2bfloat16_rn(g[i]);
+}
+
+template <typename T, int V>
+__global__ void __launch_bounds__(kThreads)
+moe_route_backward_kernel(const RouteBackwardParams p) {
+  grid_launch_dependents();
+  grid_dependency_wait();
+  const int lane = threadIdx.x & 31;
+  const int E = p.experts, K = p.top_k;
+  float c[V];
+  {
+    const int n = *p.num_tokens;
+    const float nf = static_cast<float>(n);
+    const float f = p.dloss && n > 0
+                        ? *p.dloss * (static_cast<float>(E) / (static_cast<float>(K) * nf * nf))
+                        : 0.0f;
+#pragma unroll
+    for (int i = 0; i < V; ++i)
+      c[i] = lane * V + i < E ? f * static_cast<float>(p.counts[lane * V + i]) : 0.0f;
+  }
+  const int64_t stride = static_cast<int64_t>(gridDim.x) * kWarps;
+  for (int64_t t = static_cast<int64_t>(blockIdx.x) * kWarps + (threadIdx.x >> 5); t < p.tokens;
+       t += stride) {
+    const int my_idx = lane < K ? p.idx[t * K + lane] : -1;
+    float g[V];
+    if (__shfl_sync(0xffffffffu, my_idx, 0) < 0) {
+#pragma unroll
+      for (int i = 0; i < V; ++i) g[i] = 0.0f;
+    } else {
+      const float w = my_idx >= 0 ? p.weights[t * K + lane] : 0.0f;
+      const float dw = my_idx >= 0 && p.dweights ? p.dweights[t * K + lane] : 0.0f;
+      load_row<V>(static_cast<const T *>(p.logits) + t * p.ld, E, p.vec != 0, g);
+      float xmax = -INFINITY;
+#pragma unroll
+      for (int i = 0; i < V; ++i) xmax = fmaxf(xmax, g[i]);
+#pragma unroll
+      for (int o = 16; o > 0; o >>= 1) xmax = fmaxf(xmax, __shfl_xor_sync(0xffffffffu, xmax, o));
+      float sum = 0.0f, pc = 0.0f;
+#pragma unroll
+      for (int i = 0; i < V; ++i) {
+        g[i] = expf(g[i] - xmax);
+        sum += g[i];
+        pc += g[i] * c[i];
+      }
+      const float inv = 1.0f / warp_sum(sum);
+      const float wdw = warp_sum(w * dw);
+      // what every expert's probability is multiplied by, less its own c
+      const float minus = warp_sum(pc) * inv + (p.normalize ? 0.0f : wdw);
+      const float dv = p.normalize ? w * (dw - wdw) : w * dw;
+#pragma unroll
+      for (int i = 0; i < V; ++i) g[i] = g[i] * inv * (c[i] - minus);
+      for (int j = 0; j < K; ++j) {
+        const int e = __shfl_sync(0xffffffffu, my_idx, j) - lane * V;
+        const float v = __shfl_sync(0xffffffffu, dv, j);
+#pragma unroll
+        for (int i = 0; i < V; ++i) g[i] += e == i ? v : 0.0f;
+      }
+    }
+    store_row<V>(static_cast<T *>(p.dlogits) + t * E, E, p.vec != 0, g);
+  }
+}
+
+int check_device() {
+  const DeviceInfo *d = device_info();
+  if (!d) return DG_ERR_CUDA;
+  return d->ok ? DG_OK : DG_ERR_UNSUPPORTED_ARCH;
+}
+
+int route_blocks(int64_t tokens, int num_sms) {
+  if (tokens <= kSingleBlockTokens) return 1;
+  const int64_t want = (tokens + kWarps - 1) / kWarps;
+  const int64_t most = num_sms < kMaxBlocks ? num_sms : kMaxBlocks;
+  return static_cast<int>(want < most ? want : most);
+}
+
+// Experts per lane: the power of two that covers E with 32 lanes.
+int per_lane(int experts) {
+  int v = 1;
+  while (32 * v < experts) v *= 2;
+  return v;
+}
+
+// Whether a row's V-element pieces can be loaded whole: they start on a
+// 16-byte boundary (their own size, if less) and none is cut by E.
+int vector_rows(const void *a, const void *b, int64_t ld, int64_t ld_b, int experts, int esz) {
+  const int v = per_lane(experts);
+  const int64_t bytes = v * esz < 16 ? v * esz : 16;
+  return v >= 2 && experts % v == 0 && (ld * esz) % bytes == 0 && (ld_b * esz) % bytes == 0 &&
+         reinterpret_cast<uintptr_t>(a) % bytes == 0 && reinterpret_cast<uintptr_t>(b) % bytes == 0;
+}
+
+template <typename P>
+int launch(void (*kern)(P), int blocks, int smem, const P &p, cudaStream_t stream) {
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3(blocks);
+  cfg.blockDim = dim3(kThreads);
+  cfg.dynamicSmemBytes = smem;
+  cfg.stream = stream;
+  cudaLaunchAttribute attr[1] = {pdl_attribute()};
+  cfg.attrs = attr;
+  cfg.numAttrs = 1;
+  // (a maximum of more than 48 KB has to be asked for, on each device)
+  if (smem > 48 * 1024 &&
+      cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, smem) != cudaSuccess)
+    return DG_ERR_CUDA;
+  return cudaLaunchKernelEx(&cfg, kern, p) == cudaSuccess ? DG_OK : DG_ERR_CUDA;
+}
+
+template <typename T, int V>
+int route_instance(const RouteParams &p, int blocks, cudaStream_t stream) {
+  const int smem = (kWarps + 1) * p.experts * 4;
+  return blocks == 1 ? launch(moe_route_kernel<T, V, true>, 1, smem, p, stream)
+                     : launch(moe_route_kernel<T, V, false>, blocks, smem, p, stream);
+}
+
+template <typename T>
+int route_typed(const RouteParams &p, int blocks, cudaStream_t stream) {
+  switch (per_lane(p.experts)) {
+    case 1: return route_instance<T, 1>(p, blocks, stream);
+    case 2: return route_instance<T, 2>(p, blocks, stream);
+    case 4: return route_instance<T, 4>(p, blocks, stream);
+    case 8: return route_instance<T, 8>(p, blocks, stream);
+    case 16: return route_instance<T, 16>(p, blocks, stream);
+    default: return route_instance<T, 32>(p, blocks, stream);
+  }
+}
+
+template <typename T>
+int backward_typed(const RouteBackwardParams &p, int blocks, cudaStream_t stream) {
+  switch (per_lane(p.experts)) {
+    case 1: return launch(moe_route_backward_kernel<T, 1>, blocks, 0, p, stream);
+    case 2: return launch(moe_route_backward_kernel<T, 2>, blocks, 0, p, stream);
+    case 4: return launch(moe_route_backward_kernel<T, 4>, blocks, 0, p, stream);
+    case 8: return launch(moe_route_backward_kernel<T, 8>, blocks, 0, p, stream);
+    case 16: return launch(moe_route_backward_kernel<T, 16>, blocks, 0, p, stream);
+    default: return launch(moe_route_backward_kernel<T, 32>, blocks, 0, p, stream);
+  }
+}
+
+int check_shape(int dtype, int64_t tokens, int experts, int64_t ld, int top_k, int normalize) {
+  if (dtype != DG_DTYPE_F32 && dtype != DG_DTYPE_BF16) return DG_ERR_INVALID_ARG;
+  if (normalize != 0 && normalize != 1) return DG_ERR_INVALID_ARG;
+  if (tokens < 0 || tokens > 0x7FFFFFFF || experts < 1 || experts > kMaxExperts)
+    return DG_ERR_INVALID_ARG;
+  if (top_k < 1 || top_k > kMaxTopK || top_k > experts) return DG_ERR_INVALID_ARG;
+  if (ld < experts || ld > 0x7FFFFFFF) return DG_ERR_INVALID_ARG;
+  return DG_OK;
+}
+
+bool aligned(const void *p, int n) { return reinterpret_cast<uintptr_t>(p) % n == 0; }
+
+}  // namespace
+
+}  // namespace dg
+
+extern "C" size_t dg_moe_route_workspace_size(int64_t T, int E) {
+  using namespace dg;
+  if (T <= kSingleBlockTokens || E < 1) return 0;
+  int sms = effective_num_sms();
+  if (sms <= 0) sms = kMaxBlocks;  // no usable device: size for a full B200
+  const size_t blocks = static_cast<size_t>(route_blocks(T, sms));
+  return blocks * static_cast<size_t>(E) * 8 + blocks * 4;
+}
+
+extern "C" int dg_moe_route(const void *logits, int dtype, int64_t T, int E, int64_t ld,
+                            int top_k, int normalize, const uint8_t *token_mask, int32_t *idx,
+                            float *weights, int32_t *counts, float *loss, int32_t *num_tokens,
+                            void *workspace, size_t workspace_bytes, dg_stream_t stream) {
+  using namespace dg;
+  int rc = check_shape(dtype, T, E, ld, top_k, normalize);
+  if (rc) return rc;
+  if (!counts || !loss || !num_tokens) return DG_ERR_INVALID_ARG;
+  if (T > 0 && (!logits || !idx || !weights)) return DG_ERR_INVALID_ARG;
+  if (!aligned(logits, dtype == DG_DTYPE_F32 ? 4 : 2) || !aligned(idx, 4) ||
+      !aligned(weights, 4) || !aligned(counts, 4) || !aligned(loss, 4) ||
+      !aligned(num_tokens, 4) || !aligned(workspace, 16))
+    return DG_ERR_ALIGNMENT;
+  rc = check_device();
+  if (rc) return rc;
+  const int blocks = route_blocks(T, effective_num_sms());
+  if (blocks > 1 && (!workspace || workspace_bytes < dg_moe_route_workspace_size(T, E)))
+    return DG_ERR_WORKSPACE;
+  RouteParams p{};
+  p.logits = logits;
+  p.tokens = T;
+  p.ld = ld;
+  p.experts = E;
+  p.top_k = top_k;
+  p.normalize = normalize;
+  p.vec = vector_rows(logits, logits, ld, ld, E, dtype == DG_DTYPE_F32 ? 4 : 2);
+  p.mask = token_mask;
+  p.idx = idx;
+  p.weights = weights;
+  p.counts = counts;
+  p.loss = loss;
+  p.num_tokens = num_tokens;
+  p.part_psum = static_cast<float *>(workspace);
+  p.part_counts = reinterpret_cast<int32_t *>(p.part_psum + static_cast<size_t>(blocks) * E);
+  p.status = device_info()->status;
+  cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
+  rc = dtype == DG_DTYPE_F32 ? route_typed<float>(p, blocks, s)
+                             : route_typed<__nv_bfloat16>(p, blocks, s);
+  if (rc || blocks == 1) return rc;
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3(1);
+  cfg.blockDim = dim3(kThreads);
+  cfg.stream = s;
+  cudaLaunchAttribute attr[1] = {pdl_attribute()};
+  cfg.attrs = attr;
+  cfg.numAttrs = 1;
+  return cudaLaunchKernelEx(&cfg, moe_route_finish_kernel, p, blocks) == cudaSuccess
+             ? DG_OK
+             : DG_ERR_CUDA;
+}
+
+extern "C" int dg_moe_route_backward(const void *logits, int dtype, int64_t T, int E, int64_t ld,
+                                     int top_k, int normalize, const int32_t *idx,
+                                     const float *weights, const int32_t *counts,
+                                     const int32_t *num_tokens, const float *dweights,
+                                     const float *dloss, void *dlogits, dg_stream_t stream) {
+  using namespace dg;
+  int rc = check_shape(dtype, T, E, ld, top_k, normalize);
+  if (rc) return rc;
+  if (T == 0) return DG_OK;
+  if (!logits || !idx || !weights || !counts || !num_tokens || !dlogits)
+    return DG_ERR_INVALID_ARG;
+  const int esz = dtype == DG_DTYPE_F32 ? 4 : 2;
+  if (!aligned(logits, esz) || !aligned(dlogits, esz) || !aligned(idx, 4) ||
+      !aligned(weights, 4) || !aligned(counts, 4) || !aligned(num_tokens, 4) ||
+      !aligned(dweights, 4) || !aligned(dloss, 4))
+    return DG_ERR_ALIGNMENT;
+  rc = check_device();
+  if (rc) return rc;
+  RouteBackwardParams p{};
+  p.logits = logits;
+  p.tokens = T;
+  p.ld = ld;
+  p.experts = E;
+  p.top_k = top_k;
+  p.normalize = normalize;
+  p.vec = vector_rows(logits, dlogits, ld, E, E, esz);
+  p.idx = idx;
+  p.weights = weights;
+  p.counts = counts;
+  p.num_tokens = num_tokens;
+  p.dweights = dweights;
+  p.dloss = dloss;
+  p.dlogits = dlogits;
+  // four resident blocks per SM
+  const int64_t want = (T + kWarps - 1) / kWarps;
+  const int64_t most = static_cast<int64_t>(effective_num_sms()) * 4;
+  const int blocks = static_cast<int>(want < most ? want : most);
+  cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
+  return dtype == DG_DTYPE_F32 ? backward_typed<float>(p, blocks, s)
+                               : backward_typed<__nv_bfloat16>(p, blocks, s);
+}

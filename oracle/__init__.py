@@ -30,10 +30,13 @@ Modules
            contiguous and masked forms and the k-grouped contiguous form.
 ``ue8m0``  UE8M0 (power-of-two) scale codes and the packed 4-per-int32,
            MN-major scale layout.
+``mxfp4``  E2M1 codes with a UE8M0 scale per 32 elements: quantization, values,
+           scale-word layout.
+``route``  softmax top-k routing, per-expert counts, balance loss, gradients.
 
 Every function is pinned by ``tests/test_oracle_*.py`` against something other
 than itself (closed forms, brute force, library conversions, the page's worked
 exercise).  No function here is "parity unpinned".
 """
 
-from . import bf16, e4m3, gemm, quant, ue8m0  # noqa: F401
+from . import bf16, e4m3, gemm, mxfp4, quant, route, ue8m0  # noqa: F401

@@ -1,0 +1,350 @@
+"""MXFP4 quantizers and products on the GPU against the float64 oracle.
+
+Tolerances.  Quantizer codes, scale words and read-back values are exact.  A
+product's BF16 result o is within 2^-8 |o| of the exact value by its rounding,
+plus the FP32 accumulation: K/64 tensor-core steps of 64 products each; a step
+aligns its terms and adds to the accumulator with at least 23 bits kept, so each
+of the K/64 + 64 roundings of an element loses at most 2^-23 of the sum S of its
+terms' magnitudes.
+"""
+
+import numpy as np
+import pytest
+import torch
+
+import moe_grouped_gemm_act_b200 as dg
+from moe_grouped_gemm_act_b200 import inputs
+from oracle import mxfp4
+from tests._helpers import dev
+
+pytestmark = pytest.mark.gpu
+SENTINEL = 0x7FC1
+
+
+def sentinel(*shape):
+    return torch.full(shape, SENTINEL, dtype=torch.int16, device="cuda").view(torch.bfloat16)
+
+
+def untouched(d):
+    return bool((d.view(torch.int16) == SENTINEL).all())
+
+
+def operand(x):
+    """(q, sf) on the device and the values in float64 on the device, from the oracle."""
+    codes, byte = mxfp4.quantize(x)
+    if x.ndim == 3:
+        sf = np.stack([mxfp4.scale_words(b) for b in byte])
+    else:
+        sf = mxfp4.scale_words(byte)
+    return dev(mxfp4.pack(codes)), dev(sf), dev(mxfp4.values(codes, byte))
+
+
+def check(d, a, b, what=""):
+    want, s = a @ b.T, a.abs() @ b.abs().T
+    steps = a.shape[1] / 64 + 64
+    diff = (d.double() - want).abs()
+    bound = 2.0 ** -8 * want.abs() + steps * 2.0 ** -23 * s
+    assert bool(torch.isfinite(d).all()), what
+    assert bool((diff <= bound).all()), f"{what}: {(diff - bound).max()}"
+
+
+def rnd(shape, seed, outliers=False):
+    return inputs.activations(int(np.prod(shape[:-1])), shape[-1], seed, outliers).reshape(shape)
+
+
+# ------------------------------------------------------------------ quantizers
+def special_rows(m, k, seed):
+    x = rnd((m, k), seed, outliers=True)
+    g = x.reshape(m, -1, 32)
+    g[0, 0] = 0
+    g[-1, -1] = -0.0
+    g[m // 2, 0] *= np.float32(1e-40)              # subnormal values
+    g[m // 2, -1] *= np.float32(1e37)
+    g[0, -1] = np.tile(np.array([.25, .75, 1.25, 1.75, 2.5, 3.5, 5, 6], np.float32), 4)
+    g[-1, 0] = np.float32(2.0 ** -126)
+    if m > 3:
+        g[1, 0, 5] = np.inf
+        g[2, 0, 7] = np.nan
+        g[3, 0, 1] = -np.inf
+    return x
+
+
+@pytest.mark.parametrize("dtype", [torch.float32, torch.bfloat16])
+@pytest.mark.parametrize("m,k", [(1, 32), (3, 64), (5, 96), (33, 160), (128, 128), (129, 1024),
+                                 (200, 2112), (64, 7168)])
+@pytest.mark.parametrize("transpose", [False, True])
+def test_quantize_is_exact(m, k, dtype, transpose):
+    x = torch.from_numpy(special_rows(m, k, seed=m + k)).to(dtype)
+    codes, byte = mxfp4.quantize(x.float().numpy())
+    src = (x.t() if transpose else x).contiguous().cuda()
+    q, sf = dg.dg_quantize_mxfp4(src, transpose=transpose)
+    words = mxfp4.scale_words(byte)
+    assert np.array_equal(sf.cpu().numpy(), words)
+    assert np.array_equal(q.cpu().numpy(), mxfp4.pack(codes))
+    want = mxfp4.values(codes, byte)
+    for out in (torch.float32, torch.bfloat16):
+        y = dg.dg_dequantize_mxfp4(q, sf, out)
+        assert y.dtype == out
+        # values below the type's smallest subnormal aside, both types are exact
+        assert np.array_equal(y.double().cpu().numpy(), want, equal_nan=True)
+
+
+@pytest.mark.parametrize("transpose", [False, True])
+@pytest.mark.parametrize("dtype", [torch.float32, torch.bfloat16])
+def test_quantize_strided(dtype, transpose):
+    """A view with a row stride and an offset; odd column counts when transposed."""
+    for cols, off, ld in [(96, 8, 136), (97 if transpose else 160, 8, 264), (32, 0, 40)]:
+        rows = 64
+        base = torch.from_numpy(rnd((rows, ld), 5)).to(dtype).cuda()
+        x = base[:, off:off + cols]
+        q, sf = dg.dg_quantize_mxfp4(x, transpose=transpose)
+        xx = x.float().cpu().numpy()
+        codes, byte = mxfp4.quantize(np.ascontiguousarray(xx.T if transpose else xx))
+        assert np.array_equal(q.cpu().numpy(), mxfp4.pack(codes))
+        assert np.array_equal(sf.cpu().numpy(), mxfp4.scale_words(byte))
+    # a base that only has the element's alignment
+    base = torch.from_numpy(rnd((64, 41), 6)).to(dtype).cuda()
+    if transpose:
+        x = base[:, 1:40]
+        q, sf = dg.dg_quantize_mxfp4(x, transpose=True)
+        codes, byte = mxfp4.quantize(np.ascontiguousarray(x.float().cpu().numpy().T))
+        assert np.array_equal(q.cpu().numpy(), mxfp4.pack(codes))
+    else:
+        with pytest.raises(dg.DGError):
+            dg.dg_quantize_mxfp4(base[:, 1:33])
+
+
+def test_quantize_batch_and_empty():
+    x = rnd((3, 70, 96), 7)
+    q, sf = dg.dg_quantize_mxfp4(torch.from_numpy(x).cuda())
+    assert sf.shape == (3, 1, 1, 32, 4)
+    y = dg.dg_dequantize_mxfp4(q, sf, torch.float32).cpu().numpy()
+    for b in range(3):
+        codes, byte = mxfp4.quantize(x[b])
+        assert np.array_equal(q[b].cpu().numpy(), mxfp4.pack(codes))
+        assert np.array_equal(sf[b].cpu().numpy(), mxfp4.scale_words(byte))
+        assert np.array_equal(y[b], mxfp4.values(codes, byte))
+    q, sf = dg.dg_quantize_mxfp4(torch.empty(0, 64, device="cuda"))
+    assert q.shape == (0, 32) and dg.dg_dequantize_mxfp4(q, sf).shape == (0, 64)
+
+
+# ------------------------------------------------------------------ dense product
+@pytest.mark.parametrize("m,n,k", [
+    (1, 8, 32), (1, 2112, 7168), (2, 136, 96), (5, 128, 128), (16, 256, 288), (17, 1000, 544),
+    (33, 264, 1056), (64, 7168, 2048), (100, 264, 160), (128, 256, 512), (129, 512, 1056),
+    (255, 384, 800), (256, 128, 64), (257, 1048, 1024), (300, 200, 224), (513, 2112, 736),
+    (1031, 1544, 2080), (40, 24576, 512), (4096, 2112, 512)])
+def test_gemm(m, n, k):
+    qa, sa, a = operand(rnd((m, k), m + n, outliers=True))
+    qb, sb, b = operand(inputs.weights((n, k), k + 1))
+    big = sentinel(m + 2, n)  # rows around D stay as they are
+    d = big[1:m + 1]
+    assert dg.dg_mxfp4_gemm_nt(qa, sa, qb, sb, d) is d
+    check(d, a, b, f"{m}x{n}x{k}")
+    assert untouched(big[0]) and untouched(big[-1])
+    again = torch.empty_like(d)
+    dg.dg_mxfp4_gemm_nt(qa, sa, qb, sb, again)
+    assert torch.equal(again.view(torch.int16), d.contiguous().view(torch.int16))
+    assert dg.dg_get_device_status() == 0
+
+
+@pytest.mark.parametrize("m,n,k", [(3, 264, 7168), (64, 256, 4096), (200, 256, 7168),
+                                   (600, 768, 1024)])
+def test_gemm_exact_integers(m, n, k):
+    """Unit scales and whole codes: the FP32 sums are exact, so the result is the
+    exact value's one rounding, bit for bit."""
+    g = np.random.default_rng(m)
+    ca = g.choice([0, 2, 4, 5, 10, 12], (m, k)).astype(np.uint8)
+    cb = g.choice([0, 2, 4, 10, 12, 13], (n, k)).astype(np.uint8)
+    one = lambda r: dev(mxfp4.scale_words(np.full((r, k // 32), 127, np.uint8)))
+    d = torch.empty((m, n), dtype=torch.bfloat16, device="cuda")
+    dg.dg_mxfp4_gemm_nt(dev(mxfp4.pack(ca)), one(m), dev(mxfp4.pack(cb)), one(n), d)
+    want = dev(mxfp4.VALUES[ca]) @ dev(mxfp4.VALUES[cb]).T
+    assert float(want.abs().max()) < 2 ** 24
+    assert torch.equal(d, want.float().to(torch.bfloat16))
+
+
+def test_gemm_every_scale_byte_lands_on_its_group():
+    """One nonzero product per output, with its own scales: a scale taken from
+    another row, group or operand shows."""
+    m, n, k = 130, 264, 544
+    g = np.random.default_rng(0)
+    ea, eb = g.integers(100, 150, (m, k // 32)), g.integers(100, 150, (n, k // 32))
+    for grp in (0, 1, 2, 3, 5, 8, 15, 16):
+        ca, cb = np.zeros((m, k), np.uint8), np.zeros((n, k), np.uint8)
+        ca[:, 32 * grp + 7] = 2  # 1.0
+        cb[:, 32 * grp + 7] = 4  # 2.0
+        d = torch.empty((m, n), dtype=torch.bfloat16, device="cuda")
+        dg.dg_mxfp4_gemm_nt(dev(mxfp4.pack(ca)), dev(mxfp4.scale_words(ea.astype(np.uint8))),
+                            dev(mxfp4.pack(cb)), dev(mxfp4.scale_words(eb.astype(np.uint8))), d)
+        want = np.ldexp(2.0, ea[:, grp][:, None] + eb[:, grp][None, :] - 254)
+        assert np.array_equal(d.double().cpu().numpy(), want), grp
+
+
+def test_gemm_nan_group_reaches_its_row_only():
+    x, w = rnd((40, 96), 1), inputs.weights((72, 96), 2)
+    x[7, 40] = np.nan
+    w[11, 3] = np.inf
+    qa, sa = dg.dg_quantize_mxfp4(dev(x))
+    qb, sb = dg.dg_quantize_mxfp4(dev(w))
+    d = torch.empty((40, 72), dtype=torch.bfloat16, device="cuda")
+    dg.dg_mxfp4_gemm_nt(qa, sa, qb, sb, d)
+    nan = torch.isnan(d).cpu().numpy()
+    assert nan[7].all() and nan[:, 11].all()
+    nan[7], nan[:, 11] = False, False
+    assert not nan.any()
+
+
+def test_gemm_zero_rows_and_sm_cap():
+    qa, sa, a = operand(rnd((70, 512), 3))
+    qb, sb, b = operand(inputs.weights((520, 512), 4))
+    d0 = torch.empty((0, 520), dtype=torch.bfloat16, device="cuda")
+    e, es = dg.dg_quantize_mxfp4(torch.empty(0, 512, device="cuda"))
+    dg.dg_mxfp4_gemm_nt(e, es, qb, sb, d0)
+    try:
+        for cap in (1, 7, 60):
+            dg.dg_set_num_sms(cap)
+            d = torch.empty((70, 520), dtype=torch.bfloat16, device="cuda")
+            dg.dg_mxfp4_gemm_nt(qa, sa, qb, sb, d)
+            check(d, a, b, f"cap {cap}")
+    finally:
+        dg.dg_set_num_sms(0)
+
+
+# ------------------------------------------------------------------ grouped products
+def contiguous(counts, n, k, seed, extra=0):
+    idx = []
+    for e, c in enumerate(counts):
+        idx += [e] * c + [-1] * (-c % 128)
+    idx += [-1] * extra
+    idx = np.array(idx, np.int32)
+    x = rnd((len(idx), k), seed)
+    x[idx < 0] = np.nan  # padding rows may hold anything
+    qa, sa, a = operand(x)
+    qb, sb, b = operand(inputs.weights((len(counts), n, k), seed + 1))
+    return idx, qa, sa, a, qb, sb, b
+
+
+@pytest.mark.parametrize("counts,n,k,extra", [
+    ([128], 128, 64, 0), ([1, 0, 300], 264, 160, 0), ([256, 256], 384, 512, 0),
+    ([130, 0, 0, 5, 700], 1000, 544, 256), ([0, 127, 129, 128], 72, 1056, 128),
+    ([1000, 900], 2112, 736, 0)])
+def test_contiguous(counts, n, k, extra):
+    idx, qa, sa, a, qb, sb, b = contiguous(counts, n, k, 11, extra)
+    d = sentinel(len(idx), n)
+    dg.dg_m_grouped_mxfp4_gemm_nt_contiguous(qa, sa, qb, sb, d, dev(idx))
+    for e in range(len(counts)):
+        rows = torch.from_numpy(np.flatnonzero(idx == e)).cuda()
+        if len(rows):
+            check(d[rows], a[rows], b[e], f"expert {e}")
+    assert untouched(d[torch.from_numpy(idx < 0).cuda()])
+    assert dg.dg_get_device_status() == 0
+
+
+def test_contiguous_bad_indices_are_reported():
+    idx, qa, sa, a, qb, sb, b = contiguous([256, 200], 136, 96, 13)
+    bad = idx.copy()
+    bad[5] = 1          # a block of expert 0 with a row of expert 1
+    bad[256:384] = 7    # no such expert
+    d = sentinel(len(idx), 136)
+    dg.dg_m_grouped_mxfp4_gemm_nt_contiguous(qa, sa, qb, sb, d, dev(bad))
+    assert dg.dg_get_device_status() == dg.DG_ERR_DEVICE_DATA
+    rows = torch.from_numpy(np.flatnonzero(bad == 0)).cuda()
+    check(d[rows], a[rows], b[0])
+    assert untouched(d[5]) and untouched(d[256:384])
+    assert dg.dg_get_device_status() == 0
+    d = sentinel(len(idx), 136)
+    none = np.full_like(idx, -1)
+    dg.dg_m_grouped_mxfp4_gemm_nt_contiguous(qa, sa, qb, sb, d, dev(none))
+    assert untouched(d) and dg.dg_get_device_status() == 0
+
+
+@pytest.mark.parametrize("counts,m_max,n,k", [
+    ([1], 1, 8, 32), ([0, 0], 5, 72, 96), ([3, 0, 16, 9], 16, 264, 160),
+    ([100, 1, 0, 57, 99], 100, 1000, 544), ([256, 0, 128, 129, 17], 256, 512, 1056),
+    ([300, 257, 0, 1], 300, 136, 288), ([7] * 40, 30, 128, 256)])
+def test_masked(counts, m_max, n, k):
+    g = len(counts)
+    x = rnd((g, m_max, k), 17)
+    for e, c in enumerate(counts):
+        x[e, c:] = np.nan
+    qa, sa, a = operand(x)
+    qb, sb, b = operand(inputs.weights((g, n, k), 18))
+    d = sentinel(g, m_max, n)
+    dg.dg_m_grouped_mxfp4_gemm_nt_masked(qa, sa, qb, sb, d, dev(np.array(counts, np.int32)))
+    for e, c in enumerate(counts):
+        if c:
+            check(d[e, :c], a[e, :c], b[e], f"expert {e}")
+        assert untouched(d[e, c:])
+    assert dg.dg_get_device_status() == 0
+
+
+def test_masked_bad_counts_and_graph_replay():
+    g, m_max, n, k = 4, 40, 264, 160
+    qa, sa, a = operand(rnd((g, m_max, k), 19))
+    qb, sb, b = operand(inputs.weights((g, n, k), 20))
+    mm = dev(np.array([-3, 41, 40, 0], np.int32))
+    d = sentinel(g, m_max, n)
+    dg.dg_m_grouped_mxfp4_gemm_nt_masked(qa, sa, qb, sb, d, mm)
+    assert dg.dg_get_device_status() == dg.DG_ERR_DEVICE_DATA
+    assert untouched(d[0]) and untouched(d[3])
+    check(d[1], a[1], b[1])
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        dg.dg_m_grouped_mxfp4_gemm_nt_masked(qa, sa, qb, sb, d, mm)
+    for counts in ([1, 2, 3, 4], [40, 0, 17, 33], [0, 0, 0, 0]):
+        mm.copy_(torch.tensor(counts, dtype=torch.int32))
+        d.view(torch.int16).fill_(SENTINEL)
+        graph.replay()
+        torch.cuda.synchronize()
+        for e, c in enumerate(counts):
+            if c:
+                check(d[e, :c], a[e, :c], b[e])
+            assert untouched(d[e, c:])
+    assert dg.dg_get_device_status() == 0
+
+
+def test_streams_side_by_side():
+    """Products of different shapes on two streams at once, one of them given by
+    argument; quantizers allocate for the stream they run on."""
+    s = torch.cuda.Stream()
+    x = rnd((60, 2048), 21)
+    qa, sa, a = operand(x)
+    qb, sb, b = operand(inputs.weights((1544, 2048), 22))
+    xd = dev(x)
+    d1 = [torch.empty((60, 1544), dtype=torch.bfloat16, device="cuda") for _ in range(4)]
+    d2 = [torch.empty((60, 1544), dtype=torch.bfloat16, device="cuda") for _ in range(4)]
+    torch.cuda.synchronize()
+    for i in range(4):
+        q2, s2 = dg.dg_quantize_mxfp4(xd, stream=s)
+        dg.dg_mxfp4_gemm_nt(q2, s2, qb, sb, d2[i], stream=s)
+        del q2, s2
+        dg.dg_mxfp4_gemm_nt(qa, sa, qb, sb, d1[i])
+    torch.cuda.synchronize()
+    for d in d1 + d2:
+        check(d, a, b)
+    assert dg.dg_get_device_status() == 0
+
+
+def test_backward_products_of_a_linear_layer():
+    """Y = X W^T in MXFP4; its backward products dX = dY W and dW = dY^T X with the
+    operands quantized along the axis each product contracts."""
+    m, n, k = 192, 264, 160
+    x, w, dy = rnd((m, k), 23), inputs.weights((n, k), 24), rnd((m, n), 25)
+    dy[:, 256:] = 0
+    dyd = torch.zeros(m, 288, device="cuda")      # N padded to the group size
+    dyd[:, :n] = dev(dy)
+    wt = torch.zeros(288, k, device="cuda")
+    wt[:n] = dev(w)
+    vals = lambda z: dev(mxfp4.values(*mxfp4.quantize(z)))
+    pad = lambda z, r: np.concatenate([z, np.zeros((r - z.shape[0],) + z.shape[1:], z.dtype)])
+    q1, s1 = dg.dg_quantize_mxfp4(dyd)
+    q2, s2 = dg.dg_quantize_mxfp4(wt, transpose=True)           # W^T [K, N]
+    dx = torch.empty((m, k), dtype=torch.bfloat16, device="cuda")
+    dg.dg_mxfp4_gemm_nt(q1, s1, q2, s2, dx)
+    check(dx, vals(pad(dy.T.copy(), 288).T.copy()), vals(pad(w, 288).T.copy()), "dX")
+    q3, s3 = dg.dg_quantize_mxfp4(dev(dy), transpose=True)      # dY^T [N, M]
+    q4, s4 = dg.dg_quantize_mxfp4(dev(x), transpose=True)       # X^T [K, M]
+    dw = torch.empty((n, k), dtype=torch.bfloat16, device="cuda")
+    dg.dg_mxfp4_gemm_nt(q3, s3, q4, s4, dw)
+    check(dw, vals(dy.T.copy()), vals(x.T.copy()), "dW")
