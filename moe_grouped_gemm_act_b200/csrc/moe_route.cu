@@ -40,10 +40,15 @@ constexpr int kWarps = 16;
 constexpr int kThreads = kWarps * 32;
 constexpr int kMaxExperts = 1024;
 constexpr int kMaxTopK = 32;  // lane j keeps choice j
-// Up to this many tokens one block does everything (one launch); above it a
-// second kernel joins the blocks' sums.
-constexpr int kSingleBlockTokens = 4 * kWarps;
-constexpr int kMaxBlocks = 148;
+constexpr int kFinishCtas = 8;  // one cluster
+// Up to this many tokens (four per warp of it) one cluster does everything in
+// one launch; above it a second kernel joins the blocks' sums.
+constexpr int kClusterTokens = 4 * kWarps * kFinishCtas;
+
+// Resident blocks per SM that an instance with V experts per lane is compiled
+// for: a token is a chain of shuffles and warp maxima, so warps, not
+// instructions, hide its latency.
+constexpr int resident(int v) { return v <= 4 ? 4 : v == 8 ? 3 : v == 16 ? 2 : 1; }
 
 // Order-preserving key of an FP32 value that is not NaN; -0 and +0 are one key.
 __device__ __forceinline__ uint32_t order_key(float x) {
@@ -54,6 +59,13 @@ __device__ __forceinline__ float key_value(uint32_t k) {
   return __uint_as_float((k & 0x80000000u) ? (k & 0x7FFFFFFFu) : ~k);
 }
 constexpr uint32_t kKeyNegInf = 0x007FFFFFu;  // order_key(-inf); 0: no candidate
+
+// A word of the cluster's shared memory.
+__device__ __forceinline__ uint32_t ld_shared_cluster(uint32_t addr) {
+  uint32_t v;
+  asm volatile("ld.shared::cluster.u32 %0, [%1];" : "=r"(v) : "r"(addr) : "memory");
+  return v;
+}
 
 __device__ __forceinline__ float warp_sum(float v) {
 #pragma unroll
@@ -140,50 +152,126 @@ struct RouteParams {
   int32_t *counts;
   float *loss;
   int32_t *num_tokens;
-  int32_t *part_counts;  // [blocks][E], then [blocks] routed tokens
-  float *part_psum;      // [blocks][E]
+  // [blocks][E + 1]: an expert's probability sum (FP32 bits) and count; in
+  // column E the block's routed tokens as a count
+  int2 *part;
   int *status;
 };
 
-// The sums of all blocks: counts, and the loss from the probabilities' sums.
-// `blocks` rows of E, each E consecutive; one block of kThreads threads.
-__device__ __forceinline__ void finish(const RouteParams &p, int blocks,
-                                       const int32_t *part_counts, const float *part_psum,
-                                       const int32_t *part_tokens, float *s_red) {
-  // each thread sums its experts over all blocks, in block order
-  float acc = 0.0f;
-  for (int e = threadIdx.x; e < p.experts; e += kThreads) {
-    int c = 0;
-    float s = 0.0f;
-#pragma unroll 8
-    for (int b = 0; b < blocks; ++b) {
-      c += part_counts[static_cast<int64_t>(b) * p.experts + e];
-      s += part_psum[static_cast<int64_t>(b) * p.experts + e];
-    }
-    p.counts[e] = c;
-    acc += static_cast<float>(c) * s;
-  }
-  int n = 0;
-  if (threadIdx.x < 32) {
-    for (int b = threadIdx.x; b < blocks; b += 32) n += part_tokens[b];
-    n = __reduce_add_sync(0xffffffffu, n);
-  }
-  acc = warp_sum(acc);
-  if ((threadIdx.x & 31) == 0) s_red[threadIdx.x >> 5] = acc;
-  __syncthreads();
-  if (threadIdx.x == 0) {
-    float total = 0.0f;
-    for (int w = 0; w < kWarps; ++w) total += s_red[w];
-    const float nf = static_cast<float>(n);
-    *p.loss = n > 0 ? total * (static_cast<float>(p.experts) /
-                               (static_cast<float>(p.top_k) * nf * nf))
-                    : 0.0f;
-    *p.num_tokens = n;
-  }
+__device__ __forceinline__ float loss_of(const RouteParams &p, float total, int n) {
+  const float nf = static_cast<float>(n);
+  return n > 0 ? total * (static_cast<float>(p.experts) /
+                          (static_cast<float>(p.top_k) * nf * nf))
+               : 0.0f;
 }
 
-template <typename T, int V, bool SINGLE>
-__global__ void __launch_bounds__(kThreads)
+// The choice of the k largest, one per round; no open expert left ends it.
+// (The kernel is bound by the ALU pipe -- compares, selects and integer maxima
+// -- so a round has few of them per expert.)
+//
+// FP32 logits: the maximum of the lanes' largest keys, then the lowest expert
+// among those that hold it.
+template <typename T, int V>
+struct TopK {
+  uint32_t key[V], top;
+  int at;  // the lane's lowest expert with key == top
+  __device__ __forceinline__ void find_top() {
+    top = key[0];
+#pragma unroll
+    for (int i = 1; i < V; ++i) top = max(top, key[i]);
+    at = 0;
+#pragma unroll
+    for (int i = V - 1; i >= 0; --i)
+      if (key[i] == top) at = i;
+    at += (threadIdx.x & 31) * V;
+  }
+  // Experts past E hold -inf, like closed ones.
+  __device__ __forceinline__ void init(const float x[V]) {
+#pragma unroll
+    for (int i = 0; i < V; ++i) key[i] = order_key(x[i]);
+    find_top();
+  }
+  // The row's largest logit (-inf: no expert is open).
+  __device__ __forceinline__ float largest() const {
+    return key_value(__reduce_max_sync(0xffffffffu, top));
+  }
+  // The K largest, choice j to lane j: its expert (-1: none) and logit.
+  __device__ __forceinline__ void choose(int K, int &expert, float &value) {
+    const int lane = threadIdx.x & 31;
+    uint32_t mine = kKeyNegInf;
+    expert = -1;
+    for (int j = 0; j < K; ++j) {
+      const uint32_t best = __reduce_max_sync(0xffffffffu, top);
+      if (best <= kKeyNegInf) break;  // only closed experts are left
+      const int e = static_cast<int>(__reduce_min_sync(
+          0xffffffffu, top == best ? static_cast<uint32_t>(at) : 0xFFFFFFFFu));
+      if (lane == j) {
+        expert = e;
+        mine = best;
+      }
+#pragma unroll
+      for (int i = 0; i < V; ++i)
+        if (lane * V + i == e) key[i] = 0;
+      find_top();
+    }
+    value = key_value(mine);
+  }
+};
+// BF16 logits: the 16-bit key and the expert (larger for lower experts) share a
+// 26-bit word, so all words differ and a round is one warp maximum.  The words
+// are kept relative to the last choice: chosen ones are zero or positive, the
+// others negative, that is larger as unsigned numbers, so the unsigned maximum
+// is the next choice and taking it out is one subtraction per word.
+template <int V>
+struct TopK<__nv_bfloat16, V> {
+  uint32_t rel[V], top, base;
+  __device__ __forceinline__ void find_top() {
+    top = rel[0];
+#pragma unroll
+    for (int i = 1; i + 1 < V; i += 2) top = max(max(top, rel[i]), rel[i + 1]);
+    if constexpr (V % 2 == 0) top = max(top, rel[V - 1]);
+  }
+  __device__ __forceinline__ void init(const float x[V]) {
+    const uint32_t low = 1023u - (threadIdx.x & 31) * V;
+#pragma unroll
+    for (int i = 0; i < V; ++i) {
+      const uint32_t u = __float_as_uint(x[i] + 0.0f);
+      const uint32_t flip = (static_cast<uint32_t>(static_cast<int32_t>(u) >> 31) & 0x7FFF0000u) |
+                            0x80000000u;
+      rel[i] = ((u ^ flip) >> 6) + (low - i);
+    }
+    base = 0;
+    find_top();
+  }
+  static __device__ __forceinline__ float value_of(uint32_t word) {
+    const uint32_t k = (word >> 10) << 16;
+    return key_value((k & 0x80000000u) ? k : k | 0xFFFFu);
+  }
+  __device__ __forceinline__ float largest() const {
+    return value_of(__reduce_max_sync(0xffffffffu, top));
+  }
+  __device__ __forceinline__ void choose(int K, int &expert, float &value) {
+    const int lane = threadIdx.x & 31;
+    uint32_t mine = 0x7Fu << 10;  // -inf's key is 0x7F
+    for (int j = 0; j < K; ++j) {
+      const uint32_t best = __reduce_max_sync(0xffffffffu, top);
+      base += best;
+      if (base < (0x80u << 10)) break;  // only closed experts are left
+      if (lane == j) mine = base;
+#pragma unroll
+      for (int i = 0; i < V; ++i) rel[i] -= best;
+      find_top();
+    }
+    expert = mine < (0x80u << 10) ? -1 : 1023 - static_cast<int>(mine & 1023u);
+    value = value_of(mine);
+  }
+};
+
+// CLUSTER: the grid is one cluster of kFinishCtas CTAs, whose rank 0 joins the
+// blocks' sums over the cluster's shared memory (one launch); else the sums go
+// to the workspace.
+template <typename T, int V, bool CLUSTER>
+__global__ void __launch_bounds__(kThreads, resident(V))
 moe_route_kernel(const RouteParams p) {
   extern __shared__ float s_mem[];  // [kWarps][E] probability sums, [E] counts
   __shared__ float s_red[kWarps];
@@ -203,63 +291,44 @@ moe_route_kernel(const RouteParams p) {
   for (int i = 0; i < V; ++i) psum[i] = 0.0f;
   int routed = 0;
   const int64_t stride = static_cast<int64_t>(gridDim.x) * kWarps;
-  for (int64_t t = static_cast<int64_t>(blockIdx.x) * kWarps + warp; t < p.tokens; t += stride) {
+  // (neighbouring tokens go to different blocks, so that few tokens spread)
+  for (int64_t t = static_cast<int64_t>(warp) * gridDim.x + blockIdx.x; t < p.tokens;
+       t += stride) {
     float x[V];
     load_row<V>(static_cast<const T *>(p.logits) + t * p.ld, E, p.vec != 0, x);
-    bool bad = false;
-    uint32_t key[V], top = 0;
+    TopK<T, V> topk;
+    topk.init(x);
+    const float xmax = topk.largest();
+    // a NaN or +inf anywhere makes the sum NaN, and so does a row that is
+    // closed altogether
+    float sum = 0.0f;
 #pragma unroll
     for (int i = 0; i < V; ++i) {
-      bad |= !(x[i] <= FLT_MAX);  // NaN or +inf
-      key[i] = order_key(x[i]);
-      if (lane * V + i >= E) key[i] = 0;
-      top = max(top, key[i]);
+      const float e = expf(x[i] - xmax);
+      sum += e;
+      x[i] = e;
     }
-    bad = __any_sync(0xffffffffu, bad);
-    const uint32_t first = __reduce_max_sync(0xffffffffu, top);
+    sum = warp_sum(sum);
     const bool masked = p.mask && !p.mask[t];
-    if (bad && !masked && lane == 0) record_status(p.status, DG_ERR_DEVICE_DATA);
     int my_idx = -1;
     float my_w = 0.0f;
-    if (!bad && !masked && first > kKeyNegInf) {
+    if (!masked && sum == sum) {
       ++routed;
-      const float xmax = key_value(first);
-      float sum = 0.0f;
-#pragma unroll
-      for (int i = 0; i < V; ++i) {
-        x[i] = expf(x[i] - xmax);
-        sum += x[i];
-      }
-      const float inv = 1.0f / warp_sum(sum);
+      const float inv = 1.0f / sum;
 #pragma unroll
       for (int i = 0; i < V; ++i) psum[i] += x[i] * inv;
-      uint32_t best = first;
-      for (int j = 0; j < K; ++j) {
-        if (j) best = __reduce_max_sync(0xffffffffu, top);
-        if (best <= kKeyNegInf) break;  // only closed experts are left
-        const int owner = __ffs(__ballot_sync(0xffffffffu, top == best)) - 1;
-        int at = 0;
-        if (lane == owner) {
-          bool found = false;
-          top = 0;
-#pragma unroll
-          for (int i = 0; i < V; ++i) {
-            if (!found && key[i] == best) {
-              found = true;
-              at = lane * V + i;
-              key[i] = 0;
-            }
-            top = max(top, key[i]);
-          }
-        }
-        at = __shfl_sync(0xffffffffu, at, owner);
-        if (lane == j) {
-          my_idx = at;
-          my_w = expf(key_value(best) - xmax) * inv;
-        }
-      }
+      float my_x;
+      topk.choose(K, my_idx, my_x);
+      my_w = expf(my_x - xmax) * inv;  // (0 in the lanes without a choice)
       if (p.normalize) my_w /= warp_sum(my_w);
       if (my_idx >= 0) atomicAdd(&s_counts[my_idx], 1);
+    } else if (!masked) {
+      // not routed: an error unless every logit is -inf
+      bool bad = false;
+      load_row<V>(static_cast<const T *>(p.logits) + t * p.ld, E, p.vec != 0, x);
+#pragma unroll
+      for (int i = 0; i < V; ++i) bad |= x[i] != -INFINITY;
+      if (bad) record_status(p.status, DG_ERR_DEVICE_DATA);
     }
     if (lane < K) {
       p.idx[t * K + lane] = my_idx;
@@ -271,35 +340,138 @@ moe_route_kernel(const RouteParams p) {
     if (lane * V + i < E) s_psum[warp * E + lane * V + i] = psum[i];
   if (lane == 0) atomicAdd(&s_tokens, routed);
   __syncthreads();
-  if constexpr (SINGLE) {
-    // the warps' sums first, into the first row
-    for (int e = threadIdx.x; e < E; e += kThreads) {
-      float s = 0.0f;
+  // the block's sums, in the first row (a thread reads only its own columns)
+  for (int e = threadIdx.x; e < E; e += kThreads) {
+    float s = 0.0f;
 #pragma unroll
-      for (int w = 0; w < kWarps; ++w) s += s_psum[w * E + e];
-      s_psum[e] = s;  // (only this thread reads column e)
+    for (int w = 0; w < kWarps; ++w) s += s_psum[w * E + e];
+    if constexpr (CLUSTER) {
+      s_psum[e] = s;
+    } else {
+      p.part[static_cast<int64_t>(blockIdx.x) * (E + 1) + e] =
+          make_int2(__float_as_int(s), s_counts[e]);
     }
-    finish(p, 1, s_counts, s_psum, &s_tokens, s_red);
+  }
+  if constexpr (CLUSTER) {
+    __syncwarp();
+    cluster_sync();
+    if (blockIdx.x == 0) {
+      float acc = 0.0f;
+      for (int e = threadIdx.x; e < E; e += kThreads) {
+        float s = 0.0f;
+        int c = 0;
+#pragma unroll
+        for (int r = 0; r < kFinishCtas; ++r) {
+          s += __uint_as_float(ld_shared_cluster(mapa_shared(smem_u32(s_psum + e), r)));
+          c += static_cast<int>(ld_shared_cluster(mapa_shared(smem_u32(s_counts + e), r)));
+        }
+        p.counts[e] = c;
+        acc += static_cast<float>(c) * s;
+      }
+      acc = warp_sum(acc);
+      if (lane == 0) s_red[warp] = acc;
+      __syncthreads();
+      if (threadIdx.x == 0) {
+        float total = 0.0f;
+        for (int w = 0; w < kWarps; ++w) total += s_red[w];
+        int n = 0;
+#pragma unroll
+        for (int r = 0; r < kFinishCtas; ++r)
+          n += static_cast<int>(ld_shared_cluster(mapa_shared(smem_u32(&s_tokens), r)));
+        *p.loss = loss_of(p, total, n);
+        *p.num_tokens = n;
+      }
+    }
+    __syncwarp();
+    cluster_sync();  // no CTA leaves while its sums are being read
   } else {
-    for (int e = threadIdx.x; e < E; e += kThreads) {
-      float s = 0.0f;
-#pragma unroll
-      for (int w = 0; w < kWarps; ++w) s += s_psum[w * E + e];
-      p.part_psum[static_cast<int64_t>(blockIdx.x) * E + e] = s;
-      p.part_counts[static_cast<int64_t>(blockIdx.x) * E + e] = s_counts[e];
-    }
     if (threadIdx.x == 0)
-      p.part_counts[static_cast<int64_t>(gridDim.x) * E + blockIdx.x] = s_tokens;
+      p.part[static_cast<int64_t>(blockIdx.x) * (E + 1) + E] = make_int2(0, s_tokens);
   }
 }
 
-__global__ void __launch_bounds__(kThreads)
+// Joins the blocks' sums: a cluster of kFinishCtas CTAs.  CTA c takes the blocks c,
+// c + 8, ..; its threads are `parts` rows of E + 1 columns, each summing every
+// parts-th of those blocks with kBatch loads in flight (it is bound by latency:
+// one round trip for all that fit).  The parts are added in order in shared
+// memory, then the CTAs' sums in order by CTA 0 over the cluster's.
+constexpr int kFinishThreads = 1024;
+__global__ void __launch_bounds__(kFinishThreads)
 moe_route_finish_kernel(const RouteParams p, int blocks) {
-  __shared__ float s_red[kWarps];
+  __shared__ float s_sum[kMaxExperts + kFinishThreads];
+  __shared__ int32_t s_count[kMaxExperts + kFinishThreads];
+  __shared__ float s_red[kFinishThreads / 32];
+  const int tid = threadIdx.x, cols = p.experts + 1;
+  const int parts = cols < kFinishThreads ? kFinishThreads / cols : 1;
+  constexpr int kBatch = 8;
   grid_launch_dependents();
   grid_dependency_wait();
-  finish(p, blocks, p.part_counts, p.part_psum,
-         p.part_counts + static_cast<int64_t>(blocks) * p.experts, s_red);
+  // (cols may exceed the threads by one: then each thread takes two columns)
+  for (int i = tid; i < parts * cols; i += kFinishThreads) {
+    const int part = i / cols, col = i - part * cols;
+    float s = 0.0f;
+    int c = 0;
+    for (int b0 = blockIdx.x + kFinishCtas * part; b0 < blocks;
+         b0 += kFinishCtas * parts * kBatch) {
+      int2 v[kBatch];
+#pragma unroll
+      for (int j = 0; j < kBatch; ++j) {
+        const int b = b0 + j * kFinishCtas * parts;
+        v[j] = b < blocks ? __ldcg(p.part + static_cast<int64_t>(b) * cols + col)
+                          : make_int2(0, 0);
+      }
+#pragma unroll
+      for (int j = 0; j < kBatch; ++j) {
+        s += __int_as_float(v[j].x);
+        c += v[j].y;
+      }
+    }
+    s_sum[i] = s;
+    s_count[i] = c;
+  }
+  __syncthreads();
+  for (int col = tid; col < cols; col += kFinishThreads) {
+    float s = s_sum[col];
+    int c = s_count[col];
+    for (int q = 1; q < parts; ++q) {
+      s += s_sum[q * cols + col];
+      c += s_count[q * cols + col];
+    }
+    s_sum[col] = s;  // (the first part's row; only this thread reads the column)
+    s_count[col] = c;
+  }
+  __syncwarp();
+  cluster_sync();
+  if (blockIdx.x == 0) {
+    float acc = 0.0f;
+    int n = 0;
+    for (int col = tid; col < cols; col += kFinishThreads) {
+      float s = 0.0f;
+      int c = 0;
+#pragma unroll
+      for (int r = 0; r < kFinishCtas; ++r) {
+        s += __uint_as_float(ld_shared_cluster(mapa_shared(smem_u32(s_sum + col), r)));
+        c += static_cast<int>(ld_shared_cluster(mapa_shared(smem_u32(s_count + col), r)));
+      }
+      if (col < p.experts) {
+        p.counts[col] = c;
+        acc += static_cast<float>(c) * s;
+      } else {
+        n = c;
+      }
+    }
+    acc = warp_sum(acc);
+    if ((tid & 31) == 0) s_red[tid >> 5] = acc;
+    __syncthreads();
+    if (tid == p.experts % kFinishThreads) {  // the thread that holds n
+      float total = 0.0f;
+      for (int w = 0; w < kFinishThreads / 32; ++w) total += s_red[w];
+      *p.loss = loss_of(p, total, n);
+      *p.num_tokens = n;
+    }
+  }
+  __syncwarp();
+  cluster_sync();  // no CTA leaves while its sums are being read
 }
 
 // The gradient of the logits.  A token that did not route (idx[t][0] < 0) gets
@@ -373,12 +545,15 @@ __device__ __forceinline__ void store_row(__nv_bfloat16 *row, int E, bool vec, c
 }
 
 template <typename T, int V>
-__global__ void __launch_bounds__(kThreads)
+__global__ void __launch_bounds__(kThreads, resident(V))
 moe_route_backward_kernel(const RouteBackwardParams p) {
+  // a warp's gradient row, for the chosen experts' lanes to add to
+  extern __shared__ __align__(16) float s_rows[];
   grid_launch_dependents();
   grid_dependency_wait();
   const int lane = threadIdx.x & 31;
   const int E = p.experts, K = p.top_k;
+  float *row = s_rows + (threadIdx.x >> 5) * (32 * V);
   float c[V];
   {
     const int n = *p.num_tokens;
@@ -405,8 +580,7 @@ moe_route_backward_kernel(const RouteBackwardParams p) {
       float xmax = -INFINITY;
 #pragma unroll
       for (int i = 0; i < V; ++i) xmax = fmaxf(xmax, g[i]);
-#pragma unroll
-      for (int o = 16; o > 0; o >>= 1) xmax = fmaxf(xmax, __shfl_xor_sync(0xffffffffu, xmax, o));
+      xmax = key_value(__reduce_max_sync(0xffffffffu, order_key(xmax)));
       float sum = 0.0f, pc = 0.0f;
 #pragma unroll
       for (int i = 0; i < V; ++i) {
@@ -421,12 +595,22 @@ moe_route_backward_kernel(const RouteBackwardParams p) {
       const float dv = p.normalize ? w * (dw - wdw) : w * dw;
 #pragma unroll
       for (int i = 0; i < V; ++i) g[i] = g[i] * inv * (c[i] - minus);
-      for (int j = 0; j < K; ++j) {
-        const int e = __shfl_sync(0xffffffffu, my_idx, j) - lane * V;
-        const float v = __shfl_sync(0xffffffffu, dv, j);
+      // the chosen experts are distinct, so their lanes' additions do not meet
+      store_row<V>(row, 32 * V, true, g);
+      __syncwarp();
+      if (my_idx >= 0 && my_idx < E) row[my_idx] += dv;
+      __syncwarp();
+      if constexpr (V >= 4) {
 #pragma unroll
-        for (int i = 0; i < V; ++i) g[i] += e == i ? v : 0.0f;
+        for (int i = 0; i < V; i += 4) {
+          const float4 u = *reinterpret_cast<const float4 *>(row + lane * V + i);
+          g[i] = u.x; g[i + 1] = u.y; g[i + 2] = u.z; g[i + 3] = u.w;
+        }
+      } else {
+#pragma unroll
+        for (int i = 0; i < V; ++i) g[i] = row[lane * V + i];
       }
+      __syncwarp();  // the row is free for the next token
     }
     store_row<V>(static_cast<T *>(p.dlogits) + t * E, E, p.vec != 0, g);
   }
@@ -438,18 +622,22 @@ int check_device() {
   return d->ok ? DG_OK : DG_ERR_UNSUPPORTED_ARCH;
 }
 
-int route_blocks(int64_t tokens, int num_sms) {
-  if (tokens <= kSingleBlockTokens) return 1;
-  const int64_t want = (tokens + kWarps - 1) / kWarps;
-  const int64_t most = num_sms < kMaxBlocks ? num_sms : kMaxBlocks;
-  return static_cast<int>(want < most ? want : most);
-}
-
 // Experts per lane: the power of two that covers E with 32 lanes.
 int per_lane(int experts) {
   int v = 1;
   while (32 * v < experts) v *= 2;
   return v;
+}
+
+// Blocks of a launch over `tokens`: all resident, a token per warp at least.
+int token_blocks(int64_t tokens, int experts, int num_sms) {
+  const int64_t want = (tokens + kWarps - 1) / kWarps;
+  const int64_t most = static_cast<int64_t>(num_sms) * resident(per_lane(experts));
+  return static_cast<int>(want < most ? want : most);
+}
+
+int route_blocks(int64_t tokens, int experts, int num_sms) {
+  return tokens <= kClusterTokens ? kFinishCtas : token_blocks(tokens, experts, num_sms);
 }
 
 // Whether a row's V-element pieces can be loaded whole: they start on a
@@ -462,15 +650,21 @@ int vector_rows(const void *a, const void *b, int64_t ld, int64_t ld_b, int expe
 }
 
 template <typename P>
-int launch(void (*kern)(P), int blocks, int smem, const P &p, cudaStream_t stream) {
+int launch(void (*kern)(P), int blocks, int smem, const P &p, cudaStream_t stream,
+           int cluster = 1) {
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = dim3(blocks);
   cfg.blockDim = dim3(kThreads);
   cfg.dynamicSmemBytes = smem;
   cfg.stream = stream;
-  cudaLaunchAttribute attr[1] = {pdl_attribute()};
+  cudaLaunchAttribute attr[2];
+  attr[0] = pdl_attribute();
+  attr[1].id = cudaLaunchAttributeClusterDimension;
+  attr[1].val.clusterDim.x = cluster;
+  attr[1].val.clusterDim.y = 1;
+  attr[1].val.clusterDim.z = 1;
   cfg.attrs = attr;
-  cfg.numAttrs = 1;
+  cfg.numAttrs = cluster > 1 ? 2 : 1;
   // (a maximum of more than 48 KB has to be asked for, on each device)
   if (smem > 48 * 1024 &&
       cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, smem) != cudaSuccess)
@@ -479,33 +673,38 @@ int launch(void (*kern)(P), int blocks, int smem, const P &p, cudaStream_t strea
 }
 
 template <typename T, int V>
-int route_instance(const RouteParams &p, int blocks, cudaStream_t stream) {
+int route_instance(const RouteParams &p, int blocks, bool cluster, cudaStream_t stream) {
   const int smem = (kWarps + 1) * p.experts * 4;
-  return blocks == 1 ? launch(moe_route_kernel<T, V, true>, 1, smem, p, stream)
-                     : launch(moe_route_kernel<T, V, false>, blocks, smem, p, stream);
+  return cluster ? launch(moe_route_kernel<T, V, true>, blocks, smem, p, stream, blocks)
+                 : launch(moe_route_kernel<T, V, false>, blocks, smem, p, stream);
 }
 
 template <typename T>
-int route_typed(const RouteParams &p, int blocks, cudaStream_t stream) {
+int route_typed(const RouteParams &p, int blocks, bool cluster, cudaStream_t stream) {
   switch (per_lane(p.experts)) {
-    case 1: return route_instance<T, 1>(p, blocks, stream);
-    case 2: return route_instance<T, 2>(p, blocks, stream);
-    case 4: return route_instance<T, 4>(p, blocks, stream);
-    case 8: return route_instance<T, 8>(p, blocks, stream);
-    case 16: return route_instance<T, 16>(p, blocks, stream);
-    default: return route_instance<T, 32>(p, blocks, stream);
+    case 1: return route_instance<T, 1>(p, blocks, cluster, stream);
+    case 2: return route_instance<T, 2>(p, blocks, cluster, stream);
+    case 4: return route_instance<T, 4>(p, blocks, cluster, stream);
+    case 8: return route_instance<T, 8>(p, blocks, cluster, stream);
+    case 16: return route_instance<T, 16>(p, blocks, cluster, stream);
+    default: return route_instance<T, 32>(p, blocks, cluster, stream);
   }
+}
+
+template <typename T, int V>
+int backward_instance(const RouteBackwardParams &p, int blocks, cudaStream_t stream) {
+  return launch(moe_route_backward_kernel<T, V>, blocks, kWarps * 32 * V * 4, p, stream);
 }
 
 template <typename T>
 int backward_typed(const RouteBackwardParams &p, int blocks, cudaStream_t stream) {
   switch (per_lane(p.experts)) {
-    case 1: return launch(moe_route_backward_kernel<T, 1>, blocks, 0, p, stream);
-    case 2: return launch(moe_route_backward_kernel<T, 2>, blocks, 0, p, stream);
-    case 4: return launch(moe_route_backward_kernel<T, 4>, blocks, 0, p, stream);
-    case 8: return launch(moe_route_backward_kernel<T, 8>, blocks, 0, p, stream);
-    case 16: return launch(moe_route_backward_kernel<T, 16>, blocks, 0, p, stream);
-    default: return launch(moe_route_backward_kernel<T, 32>, blocks, 0, p, stream);
+    case 1: return backward_instance<T, 1>(p, blocks, stream);
+    case 2: return backward_instance<T, 2>(p, blocks, stream);
+    case 4: return backward_instance<T, 4>(p, blocks, stream);
+    case 8: return backward_instance<T, 8>(p, blocks, stream);
+    case 16: return backward_instance<T, 16>(p, blocks, stream);
+    default: return backward_instance<T, 32>(p, blocks, stream);
   }
 }
 
@@ -527,11 +726,11 @@ bool aligned(const void *p, int n) { return reinterpret_cast<uintptr_t>(p) % n =
 
 extern "C" size_t dg_moe_route_workspace_size(int64_t T, int E) {
   using namespace dg;
-  if (T <= kSingleBlockTokens || E < 1) return 0;
+  if (T <= kClusterTokens || E < 1) return 0;
   int sms = effective_num_sms();
-  if (sms <= 0) sms = kMaxBlocks;  // no usable device: size for a full B200
-  const size_t blocks = static_cast<size_t>(route_blocks(T, sms));
-  return blocks * static_cast<size_t>(E) * 8 + blocks * 4;
+  if (sms <= 0) sms = 148;  // no usable device: size for a full B200
+  const size_t blocks = static_cast<size_t>(route_blocks(T, E, sms));
+  return blocks * (static_cast<size_t>(E) + 1) * sizeof(int2);
 }
 
 extern "C" int dg_moe_route(const void *logits, int dtype, int64_t T, int E, int64_t ld,
@@ -549,8 +748,9 @@ extern "C" int dg_moe_route(const void *logits, int dtype, int64_t T, int E, int
     return DG_ERR_ALIGNMENT;
   rc = check_device();
   if (rc) return rc;
-  const int blocks = route_blocks(T, effective_num_sms());
-  if (blocks > 1 && (!workspace || workspace_bytes < dg_moe_route_workspace_size(T, E)))
+  const int blocks = route_blocks(T, E, effective_num_sms());
+  const bool cluster = T <= kClusterTokens;
+  if (!cluster && (!workspace || workspace_bytes < dg_moe_route_workspace_size(T, E)))
     return DG_ERR_WORKSPACE;
   RouteParams p{};
   p.logits = logits;
@@ -566,20 +766,24 @@ extern "C" int dg_moe_route(const void *logits, int dtype, int64_t T, int E, int
   p.counts = counts;
   p.loss = loss;
   p.num_tokens = num_tokens;
-  p.part_psum = static_cast<float *>(workspace);
-  p.part_counts = reinterpret_cast<int32_t *>(p.part_psum + static_cast<size_t>(blocks) * E);
+  p.part = static_cast<int2 *>(workspace);
   p.status = device_info()->status;
   cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
-  rc = dtype == DG_DTYPE_F32 ? route_typed<float>(p, blocks, s)
-                             : route_typed<__nv_bfloat16>(p, blocks, s);
-  if (rc || blocks == 1) return rc;
+  rc = dtype == DG_DTYPE_F32 ? route_typed<float>(p, blocks, cluster, s)
+                             : route_typed<__nv_bfloat16>(p, blocks, cluster, s);
+  if (rc || cluster) return rc;
   cudaLaunchConfig_t cfg = {};
-  cfg.gridDim = dim3(1);
-  cfg.blockDim = dim3(kThreads);
+  cfg.gridDim = dim3(kFinishCtas);
+  cfg.blockDim = dim3(kFinishThreads);
   cfg.stream = s;
-  cudaLaunchAttribute attr[1] = {pdl_attribute()};
+  cudaLaunchAttribute attr[2];
+  attr[0] = pdl_attribute();
+  attr[1].id = cudaLaunchAttributeClusterDimension;
+  attr[1].val.clusterDim.x = kFinishCtas;
+  attr[1].val.clusterDim.y = 1;
+  attr[1].val.clusterDim.z = 1;
   cfg.attrs = attr;
-  cfg.numAttrs = 1;
+  cfg.numAttrs = 2;
   return cudaLaunchKernelEx(&cfg, moe_route_finish_kernel, p, blocks) == cudaSuccess
              ? DG_OK
              : DG_ERR_CUDA;
@@ -618,10 +822,7 @@ extern "C" int dg_moe_route_backward(const void *logits, int dtype, int64_t T, i
   p.dweights = dweights;
   p.dloss = dloss;
   p.dlogits = dlogits;
-  // four resident blocks per SM
-  const int64_t want = (T + kWarps - 1) / kWarps;
-  const int64_t most = static_cast<int64_t>(effective_num_sms()) * 4;
-  const int blocks = static_cast<int>(want < most ? want : most);
+  const int blocks = token_blocks(T, E, effective_num_sms());
   cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
   return dtype == DG_DTYPE_F32 ? backward_typed<float>(p, blocks, s)
                                : backward_typed<__nv_bfloat16>(p, blocks, s);

@@ -260,7 +260,7 @@ mxfp4_gemm_kernel(const __grid_constant__ CUtensorMap tmap_a,
       for (int ks = t.k_begin; ks < t.k_end; ++ks, ++it) {
         const int s = it % p.stages;
         if (!mbar_wait(empty_bar(s), ((it / p.stages) & 1) ^ 1, abort, p.status)) return false;
-        if (lane == 0) {
+        if (elect_one()) {
           const uint32_t sb = base + static_cast<uint32_t>(s) * stage_bytes;
           const uint32_t sf = sf_base + static_cast<uint32_t>(s) * sf_stage;
           const uint32_t sf_bytes = static_cast<uint32_t>(
@@ -299,7 +299,7 @@ mxfp4_gemm_kernel(const __grid_constant__ CUtensorMap tmap_a,
         const int s = it % p.stages;
         if (!mbar_wait(full_bar(s), (it / p.stages) & 1, abort, p.status)) return false;
         tc_fence_after();
-        if (lane == 0) {
+        if (elect_one()) {
           const uint32_t sb = base + static_cast<uint32_t>(s) * stage_bytes;
           const uint32_t sf = sf_base + static_cast<uint32_t>(s) * sf_stage;
           const uint32_t slot = tmem + kSfCol + static_cast<uint32_t>(it % kSfSlots) * kSfSlotCols;
@@ -329,7 +329,7 @@ mxfp4_gemm_kernel(const __grid_constant__ CUtensorMap tmap_a,
       return true;
     });
     // every MMA issued above completes before TMEM is freed
-    if (lane == 0) umma_commit(drain_bar);
+    if (elect_one()) umma_commit(drain_bar);
     __syncwarp();
     volatile int never = 0;
     mbar_wait(drain_bar, 0, &never, p.status);
