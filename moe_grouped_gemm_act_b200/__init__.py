@@ -659,7 +659,9 @@ _DTYPES = {torch.float32: DG_DTYPE_F32, torch.bfloat16: DG_DTYPE_BF16}
 def _on_device(name, fn_args, *ts, stream=None):
     """Calls entry point `name` with fn_args and the stream, on the device that
     the tensors ts (None allowed) share: their own current stream if none is
-    given, whatever device is current."""
+    given, whatever device is current.  (The raw-stream and current-device
+    lookups are the ones under torch.cuda's, without their argument handling,
+    which took a third of a small call.)"""
     dev = None
     for t in ts:
         if t is None:
@@ -671,16 +673,27 @@ def _on_device(name, fn_args, *ts, stream=None):
         elif t.device != dev:
             raise ValueError(f"tensors on {dev} and {t.device}: all must be on one device")
     if stream is None:
-        stream = torch.cuda.current_stream(dev)
+        raw = torch._C._cuda_getCurrentRawStream(dev.index)
     elif stream.device != dev:
         raise ValueError(f"the stream is on {stream.device}, the tensors on {dev}")
-    fn = getattr(load_library(), name)
-    if torch.cuda.current_device() == dev.index:
-        rc = fn(*fn_args, stream.cuda_stream)
+    else:
+        raw = stream.cuda_stream
+    fn = getattr(_lib or load_library(), name)
+    if torch._C._cuda_getDevice() == dev.index:
+        rc = fn(*fn_args, raw)
     else:
         with torch.cuda.device(dev):
-            rc = fn(*fn_args, stream.cuda_stream)
-    _check(rc, name)
+            rc = fn(*fn_args, raw)
+    if rc != DG_OK:
+        raise DGError(rc, name)
+
+
+def _exact(t, name, dtype, shape):
+    """_expect for a contiguous tensor of exactly this shape, quick where it holds."""
+    if t is None or t.dtype is not dtype or t.shape != shape:
+        _expect(t, name, dtype, shape)
+    if not t.is_contiguous():
+        raise ValueError("tensors must be contiguous")
 
 
 def _empty(shape, dtype, device, stream):
@@ -742,9 +755,8 @@ def dg_quantize_mxfp4(x: torch.Tensor, transpose: bool = False, q=None, sf=None,
         q = _empty(lead + (m, k // 2), torch.uint8, x.device, stream)
     if sf is None:
         sf = _empty(lead + _mx_scales(m, k), torch.int32, x.device, stream)
-    _contiguous(q, sf)
-    _expect(q, "q", torch.uint8, lead + (m, k // 2))
-    _expect(sf, "sf", torch.int32, lead + _mx_scales(m, k))
+    _exact(q, "q", torch.uint8, lead + (m, k // 2))
+    _exact(sf, "sf", torch.int32, lead + _mx_scales(m, k))
     _on_device("dg_quantize_mxfp4",
                (_ptr(x), _DTYPES[x.dtype], lead[0] if lead else 1, m, k, ld, int(transpose),
                 _ptr(q), _ptr(sf)), x, q, sf, stream=stream)
@@ -769,10 +781,9 @@ def dg_dequantize_mxfp4(q: torch.Tensor, sf: torch.Tensor, dtype: torch.dtype = 
         raise ValueError("an empty batch")
     if out is None:
         out = _empty(lead + (m, k), dtype, q.device, stream)
-    _contiguous(q, sf, out)
-    _expect(q, "q", torch.uint8, lead + (m, kh))
-    _expect(sf, "sf", torch.int32, lead + _mx_scales(m, k))
-    _expect(out, "out", dtype, lead + (m, k))
+    _exact(q, "q", torch.uint8, lead + (m, kh))
+    _exact(sf, "sf", torch.int32, lead + _mx_scales(m, k))
+    _exact(out, "out", dtype, lead + (m, k))
     _on_device("dg_dequantize_mxfp4",
                (_ptr(q), _ptr(sf), lead[0] if lead else 1, m, k, _ptr(out), _DTYPES[dtype], k),
                q, sf, out, stream=stream)
@@ -780,12 +791,11 @@ def dg_dequantize_mxfp4(q: torch.Tensor, sf: torch.Tensor, dtype: torch.dtype = 
 
 
 def _mx_operands(a, sfa, b, sfb, d, m, n, k, lead_a, lead_b):
-    _contiguous(a, sfa, b, sfb, d)
-    _expect(a, "a", torch.uint8, lead_a + (m, k // 2))
-    _expect(sfa, "sfa", torch.int32, lead_a + _mx_scales(m, k))
-    _expect(b, "b", torch.uint8, lead_b + (n, k // 2))
-    _expect(sfb, "sfb", torch.int32, lead_b + _mx_scales(n, k))
-    _expect(d, "d", torch.bfloat16, lead_a + (m, n))
+    _exact(a, "a", torch.uint8, lead_a + (m, k // 2))
+    _exact(sfa, "sfa", torch.int32, lead_a + _mx_scales(m, k))
+    _exact(b, "b", torch.uint8, lead_b + (n, k // 2))
+    _exact(sfb, "sfb", torch.int32, lead_b + _mx_scales(n, k))
+    _exact(d, "d", torch.bfloat16, lead_a + (m, n))
 
 
 def dg_mxfp4_gemm_nt(a, sfa, b, sfb, d, stream=None) -> torch.Tensor:
@@ -812,8 +822,7 @@ def dg_m_grouped_mxfp4_gemm_nt_contiguous(a, sfa, b, sfb, d, m_indices,
     m, k = a.shape[0], 2 * a.shape[1]
     g, n = b.shape[:2]
     _mx_operands(a, sfa, b, sfb, d, m, n, k, (), (g,))
-    _contiguous(m_indices)
-    _expect(m_indices, "m_indices", torch.int32, (m,))
+    _exact(m_indices, "m_indices", torch.int32, (m,))
     _on_device("dg_m_grouped_mxfp4_gemm_nt_contiguous",
                (_ptr(a), _ptr(sfa), _ptr(b), _ptr(sfb), _ptr(d), _ptr(m_indices), m, n, k, g),
                a, sfa, b, sfb, d, m_indices, stream=stream)
@@ -829,8 +838,7 @@ def dg_m_grouped_mxfp4_gemm_nt_masked(a, sfa, b, sfb, d, masked_m, stream=None) 
     g, m, k = a.shape[0], a.shape[1], 2 * a.shape[2]
     n = b.shape[1]
     _mx_operands(a, sfa, b, sfb, d, m, n, k, (g,), (g,))
-    _contiguous(masked_m)
-    _expect(masked_m, "masked_m", torch.int32, (g,))
+    _exact(masked_m, "masked_m", torch.int32, (g,))
     _on_device("dg_m_grouped_mxfp4_gemm_nt_masked",
                (_ptr(a), _ptr(sfa), _ptr(b), _ptr(sfb), _ptr(d), _ptr(masked_m), g, m, n, k),
                a, sfa, b, sfb, d, masked_m, stream=stream)
@@ -860,10 +868,9 @@ def dg_moe_route(logits: torch.Tensor, top_k: int, normalize: bool = True, token
     t, e, ld = _route_logits(logits)
     dev = logits.device
     if token_mask is not None:
-        _contiguous(token_mask)
         if token_mask.dtype not in (torch.bool, torch.uint8):
             raise ValueError("token_mask must be bool or uint8")
-        _expect(token_mask, "token_mask", token_mask.dtype, (t,))
+        _exact(token_mask, "token_mask", token_mask.dtype, (t,))
     if not 1 <= top_k <= min(e, 32):
         raise ValueError(f"top_k = {top_k} must be in 1 .. min(E, 32), E = {e}")
     if not logits.is_cuda:
@@ -873,7 +880,7 @@ def dg_moe_route(logits: torch.Tensor, top_k: int, normalize: bool = True, token
     counts = _empty((e,), torch.int32, dev, stream)
     loss = _empty((1,), torch.float32, dev, stream)
     num_tokens = _empty((1,), torch.int32, dev, stream)
-    if torch.cuda.current_device() == dev.index:
+    if torch._C._cuda_getDevice() == dev.index:
         nbytes = dg_moe_route_workspace_size(t, e)
     else:
         with torch.cuda.device(dev):
@@ -895,17 +902,16 @@ def dg_moe_route_backward(logits, idx, weights, counts, num_tokens, dweights=Non
     if idx.dim() != 2:
         raise ValueError(f"idx must be [T, top_k], got shape {tuple(idx.shape)}")
     k = idx.shape[1]
-    _contiguous(idx, weights, counts, num_tokens, dweights, dloss)
-    _expect(idx, "idx", torch.int32, (t, k))
-    _expect(weights, "weights", torch.float32, (t, k))
-    _expect(counts, "counts", torch.int32, (e,))
-    _expect(num_tokens, "num_tokens", torch.int32, (1,))
+    _exact(idx, "idx", torch.int32, (t, k))
+    _exact(weights, "weights", torch.float32, (t, k))
+    _exact(counts, "counts", torch.int32, (e,))
+    _exact(num_tokens, "num_tokens", torch.int32, (1,))
     if dweights is not None:
-        _expect(dweights, "dweights", torch.float32, (t, k))
+        _exact(dweights, "dweights", torch.float32, (t, k))
     if dloss is not None:
         if dloss.numel() != 1:
             raise ValueError("dloss must have one element")
-        _expect(dloss, "dloss", torch.float32, tuple(dloss.shape))
+        _exact(dloss, "dloss", torch.float32, tuple(dloss.shape))
     dlogits = _empty((t, e), logits.dtype, logits.device, stream)
     _on_device("dg_moe_route_backward",
                (_ptr(logits), _DTYPES[logits.dtype], t, e, ld, k, int(bool(normalize)), _ptr(idx),
