@@ -126,4 +126,27 @@ __device__ __forceinline__ void umma_mxf4(uint32_t d_tmem, uint64_t a_desc, uint
       : "memory");
 }
 
+// The CTA-pair form: M = 256, rows 0-127 of A, of D and A's scales in rank 0,
+// rows 128-255 in rank 1; B split along N between the two CTAs' shared memory,
+// its scales whole in both CTAs' TMEM.  Issued by one thread of rank 0.
+__device__ __forceinline__ void umma_mxf4_pair(uint32_t d_tmem, uint64_t a_desc, uint64_t b_desc,
+                                               uint32_t idesc, uint32_t sfa, uint32_t sfb,
+                                               uint32_t half, uint32_t accumulate) {
+  asm volatile(
+      "{\n\t.reg .pred p;\n\t"
+      "setp.ne.b32 p, %4, 0;\n\t"
+      "tcgen05.mma.cta_group::2.kind::mxf4.block_scale.scale_vec::2X [%0], %1, %2, %3, [%5], "
+      "[%6], p;\n\t}" ::"r"(d_tmem),
+      "l"(a_desc), "l"(b_desc), "r"(idesc | (half << 29) | (half << 4)), "r"(accumulate),
+      "r"(sfa | (half << 30)), "r"(sfb | (half << 30))
+      : "memory");
+}
+
+// tmem_cp_32x128b_x4 in both CTAs of the pair, each from its own shared memory
+// (the same offset) to its own TMEM.  Issued by rank 0.
+__device__ __forceinline__ void tmem_cp_32x128b_x4_pair(uint32_t taddr, uint64_t src_desc) {
+  asm volatile("tcgen05.cp.cta_group::2.32x128b.warpx4 [%0], %1;" ::"r"(taddr), "l"(src_desc)
+               : "memory");
+}
+
 }  // namespace dg

@@ -51,7 +51,6 @@ constexpr int kSfSlots = 4;
 constexpr int kMinSmem = 120 * 1024;
 
 struct MxParams {
-  const uint8_t *sfa, *sfb;  // scale blocks
   uint16_t *d;
   const int32_t *m_indices, *masked_m;
   int *status;
@@ -59,10 +58,13 @@ struct MxParams {
   int n, k;
   int groups;
   int tok_tile;      // tokens per tile: 16, 32, 64, 128 or 256
-  int tok_tiles;     // dense, contiguous: ceil(rows / tok_tile)
-  int n_tiles;       // ceil(n / 128)
+  int tok_tiles;     // dense: ceil(rows / tok_tile)
+  int n_tiles;       // ceil(n / (128 * width))
+  int width;         // 128-row blocks of B per unit: 2 for the pair form and its tail
+  int unit0, units;  // dense: the units (tiles, or pairs of them) of this launch
   int stages;
   int splits;        // CTAs of a cluster that split a tile's K (dense; 1: none)
+  int tail;          // dense: this launch is the tail of another (see launch_mxfp4)
 };
 
 struct Tile {
@@ -72,50 +74,59 @@ struct Tile {
   int k_begin, k_end;  // stages
 };
 
-// The expert of a 128-row block of the contiguous layout, -1 when it is all
-// padding.  Whole warp.  With `check`, a block that mixes experts or holds an
-// index >= groups records DG_ERR_DEVICE_DATA (the rows of other experts are
-// then not written, and nothing is computed for an index out of range).
-__device__ __forceinline__ int block_expert(const MxParams &p, int block, bool check) {
-  const int lane = threadIdx.x & 31;
-  const int4 v = __ldg(reinterpret_cast<const int4 *>(p.m_indices) + block * 32 + lane);
-  const int vals[4] = {v.x, v.y, v.z, v.w};
-  int first = -1;
+// Contiguous layout: the expert of a 128-row block, its first non-negative
+// index, -1 when it is all padding or the index is out of range.  One thread;
+// the first row answers for a block that has any expert at all in nearly every
+// layout.
+__device__ __forceinline__ int block_expert(const MxParams &p, int block) {
+  int e = __ldg(p.m_indices + static_cast<int64_t>(block) * 128);
+  if (e < 0) {
+    const int4 *v = reinterpret_cast<const int4 *>(p.m_indices) + static_cast<int64_t>(block) * 32;
+    for (int i = 0; i < 32 && e < 0; i += 8) {
+      int4 w[8];
 #pragma unroll
-  for (int i = 3; i >= 0; --i)
-    if (vals[i] >= 0) first = vals[i];
-  const unsigned any = __ballot_sync(0xffffffffu, first >= 0);
-  if (!any) return -1;
-  const int e = __shfl_sync(0xffffffffu, first, __ffs(any) - 1);
-  if (check) {
-    bool bad = e >= p.groups;
+      for (int j = 0; j < 8; ++j) w[j] = __ldg(v + i + j);
 #pragma unroll
-    for (int i = 0; i < 4; ++i) bad |= vals[i] >= 0 && vals[i] != e;
-    if (__any_sync(0xffffffffu, bad) && lane == 0) record_status(p.status, DG_ERR_DEVICE_DATA);
+      for (int j = 7; j >= 0; --j) {
+        if (w[j].w >= 0) e = w[j].w;
+        if (w[j].z >= 0) e = w[j].z;
+        if (w[j].y >= 0) e = w[j].y;
+        if (w[j].x >= 0) e = w[j].x;
+      }
+    }
   }
-  return e < p.groups ? e : -1;
+  return e;
 }
 
-// Calls f(tile) for every tile of this CTA, in order; f returns false to stop.
-// Every role walks the same list.  Whole warp.
-template <int SCHED, typename F>
-__device__ __forceinline__ void for_each_tile(const MxParams &p, const int *s_prefix, bool check,
-                                              F f) {
+// What a launch's roles read about its tiles, in shared memory.  Masked:
+// prefix[e] = tiles of the experts before e.  Contiguous: count tiles, tile i
+// of list[i] = 2 * block + (two blocks ? 1 : 0), expert[block].
+struct Tables {
+  const int *prefix;
+  const int *list, *expert;
+  int count;
+};
+
+// Calls f(tile) for every tile of this CTA (or CTA pair), in order; f returns
+// false to stop.  Every role walks the same list.
+template <int SCHED, bool PAIR, typename F>
+__device__ __forceinline__ void for_each_tile(const MxParams &p, const Tables &tab, F f) {
   const int k_stages = (p.k + kStageK - 1) / kStageK;
   Tile t;
   t.k_begin = 0;
   t.k_end = k_stages;
   t.slab = t.group = 0;
+  const int rank = PAIR ? static_cast<int>(cluster_ctarank()) : 0;
   if constexpr (SCHED == kMxMasked) {
-    const int units = s_prefix[p.groups];
+    const int units = tab.prefix[p.groups];
     for (int u = blockIdx.x; u < units; u += gridDim.x) {
       int lo = 0, hi = p.groups - 1;  // largest e with prefix[e] <= u
       while (lo < hi) {
         const int mid = (lo + hi + 1) >> 1;
-        if (s_prefix[mid] <= u) lo = mid; else hi = mid - 1;
+        if (tab.prefix[mid] <= u) lo = mid; else hi = mid - 1;
       }
-      const int r = u - s_prefix[lo];
-      const int tt = (s_prefix[lo + 1] - s_prefix[lo]) / p.n_tiles;  // token tiles
+      const int r = u - tab.prefix[lo];
+      const int tt = (tab.prefix[lo + 1] - tab.prefix[lo]) / p.n_tiles;  // token tiles
       const int nt = r / tt;
       const int m = min(__ldg(p.masked_m + lo), p.rows);
       t.slab = t.group = lo;
@@ -125,66 +136,74 @@ __device__ __forceinline__ void for_each_tile(const MxParams &p, const int *s_pr
       if (!f(t)) return;
     }
   } else {
-    const int units = p.tok_tiles * p.n_tiles;
-    // (a cluster's CTAs share one tile, each a part of its K)
-    const int first = blockIdx.x / p.splits, stride = gridDim.x / p.splits;
-    if (SCHED == kMxDense && p.splits > 1) {
+    // a cluster's CTAs share a unit (a pair) or a tile (each a part of its K);
+    // `parts` tiles make up a unit of the tail of a pair launch
+    const int cluster = PAIR ? 2 : p.splits;
+    const int parts = PAIR ? 1 : p.width;
+    const int tok_tiles = SCHED == kMxContiguous ? tab.count : p.tok_tiles;
+    const int total = (SCHED == kMxContiguous ? tok_tiles * p.n_tiles : p.units) * parts;
+    const int first = blockIdx.x / cluster, stride = gridDim.x / cluster;
+    if (SCHED == kMxDense && !PAIR && p.splits > 1) {
       const int s = blockIdx.x - first * p.splits;
       t.k_begin = k_stages * s / p.splits;
       t.k_end = k_stages * (s + 1) / p.splits;
     }
-    for (int u = first; u < units; u += stride) {
+    for (int v = first; v < total; v += stride) {
+      const int u = p.unit0 + v / parts;
       // groups of kRaster token tiles, all rows of B for one after another:
       // a wave's tiles share both operands in L2
       constexpr int kRaster = 16;
       const int grp = u / (kRaster * p.n_tiles);
       const int in = u - grp * kRaster * p.n_tiles;
-      const int width = min(kRaster, p.tok_tiles - grp * kRaster);
-      const int nt = in / width;
-      t.n0 = nt * kTileN;
-      t.tok0 = (grp * kRaster + in - nt * width) * p.tok_tile;
-      t.tokens = min(p.tok_tile, p.rows - t.tok0);
+      const int across = min(kRaster, tok_tiles - grp * kRaster);
+      const int nt = in / across;
+      const int tt = grp * kRaster + in - nt * across;
+      t.n0 = (nt * p.width + (PAIR ? rank : v % parts)) * kTileN;
+      if (!PAIR && t.n0 >= p.n) continue;
       if constexpr (SCHED == kMxContiguous) {
-        // one tile for all blocks of one expert next to each other
-        const int blocks = t.tokens / 128, tok0 = t.tok0;
-        int e = block_expert(p, tok0 / 128, check);
-        int from = 0;
-        for (int b = 1; b <= blocks; ++b) {
-          const int next = b < blocks ? block_expert(p, tok0 / 128 + b, check) : -1;
-          if (next == e && b < blocks) continue;
-          if (e >= 0) {
-            t.tok0 = tok0 + from * 128;
-            t.tokens = (b - from) * 128;
-            t.group = e;
-            if (!f(t)) return;
-          }
-          from = b;
-          e = next;
-        }
+        const int entry = tab.list[tt];
+        t.tok0 = (entry >> 1) * 128;
+        t.tokens = entry & 1 ? 256 : 128;
+        t.group = tab.expert[entry >> 1];
       } else {
-        if (!f(t)) return;
+        t.tok0 = tt * p.tok_tile;
+        t.tokens = min(p.tok_tile, p.rows - t.tok0);
       }
+      if (!f(t)) return;
     }
   }
 }
 
-template <int SCHED>
+// Rows of A (MMA columns) of a tile: a multiple of 16, of 32 for the pair,
+// whose CTAs hold half of them each.
+template <bool PAIR>
+__device__ __forceinline__ int mma_n(const Tile &t) {
+  return PAIR ? (t.tokens + 31) / 32 * 32 : (t.tokens + 15) / 16 * 16;
+}
+
+// PAIR: two CTAs of a cluster compute a tile of 256 rows of B with
+// cta_group::2 MMAs issued by rank 0; each loads its 128 rows of B and half of
+// the tokens, so an SM moves 32 KB per stage instead of 48 KB.
+template <int SCHED, bool PAIR>
 __global__ void __launch_bounds__(kThreads, 1)
 mxfp4_gemm_kernel(const __grid_constant__ CUtensorMap tmap_a,
-                  const __grid_constant__ CUtensorMap tmap_b, const MxParams p) {
+                  const __grid_constant__ CUtensorMap tmap_b,
+                  const __grid_constant__ CUtensorMap tmap_sfa,
+                  const __grid_constant__ CUtensorMap tmap_sfb, const MxParams p) {
   extern __shared__ uint8_t smem_raw[];
   __shared__ __align__(8) uint64_t s_bars[2 * kMaxStages + 5];
   __shared__ uint32_t s_tmem;
+  __shared__ int s_count;
   __shared__ volatile int s_abort;
   // 1024-byte aligned base of the stage ring (the 128-byte swizzle's atom)
   const uint32_t raw = smem_u32(smem_raw);
   const uint32_t base = (raw + 1023u) & ~1023u;
-  const uint32_t a_bytes = static_cast<uint32_t>(p.tok_tile) * (kStageK / 2);
+  const uint32_t a_bytes =
+      static_cast<uint32_t>(PAIR ? p.tok_tile / 2 : p.tok_tile) * (kStageK / 2);
   const uint32_t stage_bytes = kBBytes + a_bytes;
-  const uint32_t sf_a_bytes = p.tok_tile > 128 ? 2 * kSfBBytes : kSfBBytes;
-  const uint32_t sf_stage = kSfBBytes + sf_a_bytes;
+  const uint32_t sf_stage = kSfBBytes + (p.tok_tile > 128 ? 2 * kSfBBytes : kSfBBytes);
   const uint32_t sf_base = base + static_cast<uint32_t>(p.stages) * stage_bytes;
-  int *s_prefix = reinterpret_cast<int *>(
+  int *s_table = reinterpret_cast<int *>(
       smem_raw + (sf_base - raw) + static_cast<uint32_t>(p.stages) * sf_stage);
   const uint32_t bars = smem_u32(s_bars);
   auto full_bar = [&](int s) { return bars + 8u * s; };
@@ -194,22 +213,40 @@ mxfp4_gemm_kernel(const __grid_constant__ CUtensorMap tmap_a,
   const uint32_t drain_bar = bars + 8u * (2 * kMaxStages + 4);
 
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const uint32_t rank = PAIR ? cluster_ctarank() : 0;
   const int nbuf = p.tok_tile > 128 ? 1 : 2;
   const uint32_t buf_cols = p.tok_tile > 128 ? 256u : 128u;
   const int k_words = (p.k + 127) / 128;
   const int a_blocks = (p.rows + 127) / 128, b_blocks = (p.n + 127) / 128;  // per slab / expert
+  const int blocks = p.rows / 128;  // contiguous
+  Tables tab;
+  tab.prefix = s_table;
+  tab.expert = s_table;
+  tab.list = s_table + blocks;
+  tab.count = 0;
 
-  grid_launch_dependents();
+  if (SCHED == kMxDense && warp == 3) {
+    // B's boxes of the first stages are asked into L2 before the set-up and the
+    // dependency wait (a prefetch only fills L2, which the previous kernel's
+    // writes go through as well), so HBM works meanwhile
+    for_each_tile<SCHED, PAIR>(p, tab, [&](const Tile &t) {
+      if (t.n0 < p.n && lane < p.stages && t.k_begin + lane < t.k_end)
+        tma_prefetch_3d(&tmap_b, (t.k_begin + lane) * (kStageK / 2), t.n0, t.group);
+      return false;
+    });
+  }
   if (threadIdx.x == 0) {
     prefetch_tmap(&tmap_a);
     prefetch_tmap(&tmap_b);
+    prefetch_tmap(&tmap_sfa);
+    prefetch_tmap(&tmap_sfb);
     for (int s = 0; s < p.stages; ++s) {
       mbar_init(full_bar(s), 1);
       mbar_init(empty_bar(s), 1);
     }
     for (int b = 0; b < 2; ++b) {
       mbar_init(tfull_bar(b), 1);
-      mbar_init(tempty_bar(b), kEpiWarps);
+      mbar_init(tempty_bar(b), PAIR ? 2 * kEpiWarps : kEpiWarps);
     }
     mbar_init(drain_bar, 1);
     s_abort = 0;
@@ -217,122 +254,194 @@ mxfp4_gemm_kernel(const __grid_constant__ CUtensorMap tmap_a,
     fence_proxy_async_smem();
   }
   if (warp == 1) {
-    tmem_alloc(smem_u32(&s_tmem), kTmemCols);
-    tmem_relinquish();
-  }
-  grid_dependency_wait();
-  if (SCHED == kMxMasked && warp == 2) {
-    // prefix[e]: tiles of the experts before e
-    int running = 0;
-    for (int e0 = 0; e0 < p.groups; e0 += 32) {
-      const int e = e0 + lane;
-      int v = 0;
-      if (e < p.groups) {
-        const int m = __ldg(p.masked_m + e);
-        if (m < 0 || m > p.rows) record_status(p.status, DG_ERR_DEVICE_DATA);
-        v = (min(max(m, 0), p.rows) + p.tok_tile - 1) / p.tok_tile * p.n_tiles;
-      }
-      int incl = v;
-#pragma unroll
-      for (int o = 1; o < 32; o <<= 1) {
-        const int t = __shfl_up_sync(0xffffffffu, incl, o);
-        if (lane >= o) incl += t;
-      }
-      if (e < p.groups) s_prefix[e] = running + incl - v;
-      running += __shfl_sync(0xffffffffu, incl, 31);
+    if constexpr (PAIR) {
+      tmem_alloc_pair(smem_u32(&s_tmem), kTmemCols);
+      tmem_relinquish_pair();
+    } else {
+      tmem_alloc(smem_u32(&s_tmem), kTmemCols);
+      tmem_relinquish();
     }
-    if (lane == 0) s_prefix[p.groups] = running;
+  }
+  // A tail does not read what the launch before it writes, and that launch let
+  // it start only after the kernels before both had completed; it waits for it
+  // at its own end instead, so that whatever follows the tail follows both.
+  if (!p.tail) grid_dependency_wait();
+  grid_launch_dependents();
+  if constexpr (SCHED == kMxMasked) {
+    if (warp == 2) {
+      int running = 0;
+      for (int e0 = 0; e0 < p.groups; e0 += 32) {
+        const int e = e0 + lane;
+        int v = 0;
+        if (e < p.groups) {
+          const int m = __ldg(p.masked_m + e);
+          if (m < 0 || m > p.rows) record_status(p.status, DG_ERR_DEVICE_DATA);
+          v = (min(max(m, 0), p.rows) + p.tok_tile - 1) / p.tok_tile * p.n_tiles;
+        }
+        int incl = v;
+#pragma unroll
+        for (int o = 1; o < 32; o <<= 1) {
+          const int t = __shfl_up_sync(0xffffffffu, incl, o);
+          if (lane >= o) incl += t;
+        }
+        if (e < p.groups) s_table[e] = running + incl - v;
+        running += __shfl_sync(0xffffffffu, incl, 31);
+      }
+      if (lane == 0) s_table[p.groups] = running;
+    }
+  }
+  if constexpr (SCHED == kMxContiguous) {
+    for (int b = threadIdx.x; b < blocks; b += kThreads) {
+      int e = block_expert(p, b);
+      if (e >= p.groups) {
+        record_status(p.status, DG_ERR_DEVICE_DATA);
+        e = -1;
+      }
+      s_table[b] = e;
+    }
+    __syncthreads();
+    if (warp == 2) {
+      // a tile starts at every other block (every one, for tiles of 128
+      // tokens) of a run of blocks of one expert
+      int *list = s_table + blocks;
+      int count = 0, run = 0, before = -1;  // blocks of the run that ends before b0
+      for (int b0 = 0; b0 < blocks; b0 += 32) {
+        const int b = b0 + lane;
+        const int e = b < blocks ? s_table[b] : -1;
+        const int prev = __shfl_up_sync(0xffffffffu, e, 1);
+        const bool starts = e != (lane ? prev : before);
+        const unsigned st = __ballot_sync(0xffffffffu, starts);
+        // the block's position in its run
+        const unsigned upto = st & (0xFFFFFFFFu >> (31 - lane));
+        const int pos = upto ? lane - (31 - __clz(upto)) : run + lane;
+        const bool two = p.tok_tile > 128;
+        const bool head = e >= 0 && (!two || pos % 2 == 0);
+        const unsigned heads = __ballot_sync(0xffffffffu, head);
+        if (head)
+          list[count + __popc(heads & ((1u << lane) - 1u))] =
+              2 * b + (two && b + 1 < blocks && s_table[b + 1] == e ? 1 : 0);
+        count += __popc(heads);
+        run = __shfl_sync(0xffffffffu, pos, 31) + 1;
+        before = __shfl_sync(0xffffffffu, e, 31);
+      }
+      if (lane == 0) s_count = count;
+    }
   }
   tc_fence_before();
   __syncthreads();
+  if constexpr (PAIR) cluster_sync();  // both CTAs' barriers exist before any remote use
   tc_fence_after();
+  if constexpr (SCHED == kMxContiguous) tab.count = s_count;
   const uint32_t tmem = s_tmem;
   volatile int *abort = &s_abort;
 
   if (warp == 0) {
     // ================================================================ producer
     int it = 0;
-    for_each_tile<SCHED>(p, s_prefix, true, [&](const Tile &t) {
+    for_each_tile<SCHED, PAIR>(p, tab, [&](const Tile &t) {
       const int b_block = t.group * b_blocks + t.n0 / 128;
       const int a_block = t.slab * a_blocks + t.tok0 / 128;
-      // the second row block of a 256-token tile, where the tile reaches it
-      const bool second = t.tokens > 128;
+      const int a_row = t.tok0 + static_cast<int>(rank) * (mma_n<PAIR>(t) / 2);
       for (int ks = t.k_begin; ks < t.k_end; ++ks, ++it) {
         const int s = it % p.stages;
         if (!mbar_wait(empty_bar(s), ((it / p.stages) & 1) ^ 1, abort, p.status)) return false;
         if (elect_one()) {
           const uint32_t sb = base + static_cast<uint32_t>(s) * stage_bytes;
           const uint32_t sf = sf_base + static_cast<uint32_t>(s) * sf_stage;
-          const uint32_t sf_bytes = static_cast<uint32_t>(
-              min(kStageWords, k_words - ks * kStageWords)) * kMxBlockBytes;
-          mbar_arrive_expect_tx(full_bar(s), stage_bytes + sf_bytes * (second ? 3u : 2u));
-          tma_load_3d(sb, &tmap_b, full_bar(s), ks * (kStageK / 2), t.n0, t.group);
-          tma_load_3d(sb + kBBytes, &tmap_a, full_bar(s), ks * (kStageK / 2), t.tok0, t.slab);
-          const int64_t w = static_cast<int64_t>(ks) * kStageWords;
-          bulk_load(sf, p.sfb + (static_cast<int64_t>(b_block) * k_words + w) * kMxBlockBytes,
-                    sf_bytes, full_bar(s));
-          const uint8_t *src =
-              p.sfa + (static_cast<int64_t>(a_block) * k_words + w) * kMxBlockBytes;
-          bulk_load(sf + kSfBBytes, src, sf_bytes, full_bar(s));
-          if (second)
-            bulk_load(sf + 2 * kSfBBytes, src + static_cast<int64_t>(k_words) * kMxBlockBytes,
-                      sf_bytes, full_bar(s));
+          const int kc = ks * (kStageK / 2), wc = ks * kStageWords;
+          if constexpr (PAIR) {
+            // both CTAs' boxes complete on rank 0's barrier
+            const uint32_t fb = mapa_shared(full_bar(s), 0);
+            if (rank == 0) mbar_arrive_expect_tx(full_bar(s), 2 * (stage_bytes + sf_stage));
+            tma_load_3d_pair(sb, &tmap_b, fb, kc, t.n0, t.group);
+            tma_load_3d_pair(sb + kBBytes, &tmap_a, fb, kc, a_row, t.slab);
+            tma_load_3d_pair(sf, &tmap_sfb, fb, 0, wc, b_block);
+            tma_load_3d_pair(sf + kSfBBytes, &tmap_sfa, fb, 0, wc, a_block);
+          } else {
+            mbar_arrive_expect_tx(full_bar(s), stage_bytes + sf_stage);
+            tma_load_3d(sb, &tmap_b, full_bar(s), kc, t.n0, t.group);
+            tma_load_3d(sb + kBBytes, &tmap_a, full_bar(s), kc, a_row, t.slab);
+            tma_load_3d(sf, &tmap_sfb, full_bar(s), 0, wc, b_block);
+            tma_load_3d(sf + kSfBBytes, &tmap_sfa, full_bar(s), 0, wc, a_block);
+          }
         }
         __syncwarp();
       }
       return true;
     });
     // no copy may still be writing this CTA's shared memory when it exits
+    // (pair: rank 0's barriers count both CTAs' bytes, and rank 1 leaves after
+    // rank 0 at the cluster barrier)
     volatile int never = 0;
-    for (int i = max(0, it - p.stages); i < it; ++i)
-      mbar_wait(full_bar(i % p.stages), (i / p.stages) & 1, &never, p.status);
+    if (rank == 0)
+      for (int i = max(0, it - p.stages); i < it; ++i)
+        mbar_wait(full_bar(i % p.stages), (i / p.stages) & 1, &never, p.status);
   } else if (warp == 1) {
     // ================================================================ MMA issuer
-    const int k_mmas = (p.k + kMmaK - 1) / kMmaK;
-    int it = 0, tile_i = 0;
-    for_each_tile<SCHED>(p, s_prefix, false, [&](const Tile &t) {
-      const int buf = tile_i % nbuf;
-      if (!mbar_wait(tempty_bar(buf), ((tile_i / nbuf) & 1) ^ 1, abort, p.status)) return false;
-      const uint32_t d = tmem + static_cast<uint32_t>(buf) * buf_cols;
-      const uint32_t idesc = idesc_mxf4(kTileN, (t.tokens + 15) / 16 * 16);
-      for (int ks = t.k_begin; ks < t.k_end; ++ks, ++it) {
-        const int s = it % p.stages;
-        if (!mbar_wait(full_bar(s), (it / p.stages) & 1, abort, p.status)) return false;
-        tc_fence_after();
-        if (elect_one()) {
-          const uint32_t sb = base + static_cast<uint32_t>(s) * stage_bytes;
-          const uint32_t sf = sf_base + static_cast<uint32_t>(s) * sf_stage;
-          const uint32_t slot = tmem + kSfCol + static_cast<uint32_t>(it % kSfSlots) * kSfSlotCols;
-          const int words = min(kStageWords, k_words - ks * kStageWords);
-          for (int w = 0; w < words; ++w) {
-            tmem_cp_32x128b_x4(slot + 4 * w, smem_desc_rows16(sf + kMxBlockBytes * w));
-            tmem_cp_32x128b_x4(slot + 8 + 8 * w,
-                               smem_desc_rows16(sf + kSfBBytes + kMxBlockBytes * w));
-            if (t.tokens > 128)
-              tmem_cp_32x128b_x4(slot + 12 + 8 * w,
-                                 smem_desc_rows16(sf + 2 * kSfBBytes + kMxBlockBytes * w));
-          }
-          const uint64_t bdesc = smem_desc_k128_sw128(sb);
-          const uint64_t adesc = smem_desc_k128_sw128(sb + kBBytes);
-          const int mmas = min(kStageK / kMmaK, k_mmas - ks * (kStageK / kMmaK));
+    if (rank == 0) {
+      const int k_mmas = (p.k + kMmaK - 1) / kMmaK;
+      int it = 0, tile_i = 0;
+      for_each_tile<SCHED, PAIR>(p, tab, [&](const Tile &t) {
+        const int buf = tile_i % nbuf;
+        if (!mbar_wait(tempty_bar(buf), ((tile_i / nbuf) & 1) ^ 1, abort, p.status)) return false;
+        const uint32_t d = tmem + static_cast<uint32_t>(buf) * buf_cols;
+        const uint32_t idesc = idesc_mxf4(PAIR ? 2 * kTileN : kTileN, mma_n<PAIR>(t));
+        for (int ks = t.k_begin; ks < t.k_end; ++ks, ++it) {
+          const int s = it % p.stages;
+          if (!mbar_wait(full_bar(s), (it / p.stages) & 1, abort, p.status)) return false;
+          tc_fence_after();
+          if (elect_one()) {
+            const uint32_t sb = base + static_cast<uint32_t>(s) * stage_bytes;
+            const uint32_t sf = sf_base + static_cast<uint32_t>(s) * sf_stage;
+            const uint32_t slot =
+                tmem + kSfCol + static_cast<uint32_t>(it % kSfSlots) * kSfSlotCols;
+            auto cp = [&](uint32_t to, uint32_t from) {
+              if constexpr (PAIR) tmem_cp_32x128b_x4_pair(to, smem_desc_rows16(from));
+              else tmem_cp_32x128b_x4(to, smem_desc_rows16(from));
+            };
+            const int words = min(kStageWords, k_words - ks * kStageWords);
+            for (int w = 0; w < words; ++w) {
+              cp(slot + 4 * w, sf + kMxBlockBytes * w);
+              cp(slot + 8 + 8 * w, sf + kSfBBytes + kMxBlockBytes * w);
+              if (t.tokens > 128) cp(slot + 12 + 8 * w, sf + 2 * kSfBBytes + kMxBlockBytes * w);
+            }
+            const uint64_t bdesc = smem_desc_k128_sw128(sb);
+            const uint64_t adesc = smem_desc_k128_sw128(sb + kBBytes);
+            const int mmas = min(kStageK / kMmaK, k_mmas - ks * (kStageK / kMmaK));
 #pragma unroll
-          for (int j = 0; j < kStageK / kMmaK; ++j)
-            if (j < mmas)
-              umma_mxf4(d, bdesc + 2 * j, adesc + 2 * j, idesc, slot + 4 * (j >> 1),
-                        slot + 8 + 8 * (j >> 1), 2u * (j & 1), ks > t.k_begin || j > 0 ? 1u : 0u);
-          umma_commit(empty_bar(s));
-          if (ks + 1 == t.k_end) umma_commit(tfull_bar(buf));
+            for (int j = 0; j < kStageK / kMmaK; ++j) {
+              if (j < mmas) {
+                const uint32_t more = ks > t.k_begin || j > 0 ? 1u : 0u;
+                const uint32_t sfb = slot + 4 * (j >> 1), sfa = slot + 8 + 8 * (j >> 1);
+                if constexpr (PAIR)
+                  umma_mxf4_pair(d, bdesc + 2 * j, adesc + 2 * j, idesc, sfb, sfa, 2u * (j & 1),
+                                 more);
+                else
+                  umma_mxf4(d, bdesc + 2 * j, adesc + 2 * j, idesc, sfb, sfa, 2u * (j & 1), more);
+              }
+            }
+            if constexpr (PAIR) {
+              umma_commit_pair_both(empty_bar(s));
+              if (ks + 1 == t.k_end) umma_commit_pair_both(tfull_bar(buf));
+            } else {
+              umma_commit(empty_bar(s));
+              if (ks + 1 == t.k_end) umma_commit(tfull_bar(buf));
+            }
+          }
+          __syncwarp();
         }
-        __syncwarp();
+        ++tile_i;
+        return true;
+      });
+      // every MMA issued above completes before TMEM is freed
+      if (elect_one()) {
+        if constexpr (PAIR) umma_commit_pair_own(drain_bar);
+        else umma_commit(drain_bar);
       }
-      ++tile_i;
-      return true;
-    });
-    // every MMA issued above completes before TMEM is freed
-    if (elect_one()) umma_commit(drain_bar);
-    __syncwarp();
-    volatile int never = 0;
-    mbar_wait(drain_bar, 0, &never, p.status);
+      __syncwarp();
+      volatile int never = 0;
+      mbar_wait(drain_bar, 0, &never, p.status);
+    }
   } else if (warp >= kFirstEpiWarp) {
     // ================================================================ epilogue
     // Warp w reads lanes 32 (w mod 4) .. and every other 16-column chunk; the
@@ -340,13 +449,27 @@ mxfp4_gemm_kernel(const __grid_constant__ CUtensorMap tmap_a,
     const int half = (warp - kFirstEpiWarp) >> 2;
     const int quarter = warp & 3;
     int tile_i = 0;
-    for_each_tile<SCHED>(p, s_prefix, false, [&](const Tile &t) {
+    for_each_tile<SCHED, PAIR>(p, tab, [&](const Tile &t) {
       const int buf = tile_i % nbuf;
+      // rows that are stored: bit l of live[i] is token 32 i + l
+      uint32_t live[8];
+      bool mixed = false;
+#pragma unroll
+      for (int i = 0; i < 8; ++i) {
+        bool v = 32 * i + lane < t.tokens;
+        if (SCHED == kMxContiguous && v) {
+          const int e = __ldg(p.m_indices + t.tok0 + 32 * i + lane);
+          v = e == t.group;
+          mixed |= !v && e >= 0;
+        }
+        live[i] = __ballot_sync(0xffffffffu, v);
+      }
+      if (SCHED == kMxContiguous && mixed) record_status(p.status, DG_ERR_DEVICE_DATA);
       if (!mbar_wait(tfull_bar(buf), (tile_i / nbuf) & 1, abort, p.status)) return false;
       tc_fence_after();
       const uint32_t acc = tmem + static_cast<uint32_t>(buf) * buf_cols +
                            (static_cast<uint32_t>(quarter * 32) << 16);
-      if (SCHED == kMxDense && p.splits > 1) {
+      if (SCHED == kMxDense && !PAIR && p.splits > 1) {
         // this CTA's FP32 partial goes to its stage ring (drained: all its
         // MMAs are done), [token][128]
         for (int c0 = half * 16; c0 < t.tokens; c0 += 32) {
@@ -384,15 +507,9 @@ mxfp4_gemm_kernel(const __grid_constant__ CUtensorMap tmap_a,
       }
       tc_fence_before();
       __syncwarp();
-      if (lane == 0) mbar_arrive(tempty_bar(buf));
-      // rows that are stored: bit l of live[i] is token 32 i + l
-      uint32_t live[8];
-#pragma unroll
-      for (int i = 0; i < 8; ++i) {
-        bool v = 32 * i + lane < t.tokens;
-        if (SCHED == kMxContiguous && v)
-          v = __ldg(p.m_indices + t.tok0 + 32 * i + lane) == t.group;
-        live[i] = __ballot_sync(0xffffffffu, v);
+      if (lane == 0) {
+        if constexpr (PAIR) mbar_arrive_cluster(mapa_shared(tempty_bar(buf), 0));
+        else mbar_arrive(tempty_bar(buf));
       }
       // neighbouring lanes hold neighbouring columns of D: each pair of lanes
       // swaps halves so that the even lane stores two columns of one token,
@@ -421,16 +538,16 @@ mxfp4_gemm_kernel(const __grid_constant__ CUtensorMap tmap_a,
     });
   }
 
-  if (SCHED == kMxDense && p.splits > 1) {
+  if (SCHED == kMxDense && !PAIR && p.splits > 1) {
     // ============================================================ K reduction
     // The CTAs of the cluster hold the partials of one tile: each sums a share
     // of the tokens over the cluster's shared memory, in split order.
     __syncwarp();
     cluster_sync();
-    const int rank = static_cast<int>(cluster_ctarank());
-    for_each_tile<SCHED>(p, s_prefix, false, [&](const Tile &t) {
+    const int share = static_cast<int>(cluster_ctarank());
+    for_each_tile<SCHED, PAIR>(p, tab, [&](const Tile &t) {
       const int n = t.n0 + 4 * lane;
-      for (int c = rank + p.splits * warp; c < t.tokens; c += p.splits * (kThreads / 32)) {
+      for (int c = share + p.splits * warp; c < t.tokens; c += p.splits * (kThreads / 32)) {
         const uint32_t at = base + static_cast<uint32_t>(c * kTileN + 4 * lane) * 4u;
         float4 v[8];
 #pragma unroll
@@ -457,8 +574,15 @@ mxfp4_gemm_kernel(const __grid_constant__ CUtensorMap tmap_a,
 
   tc_fence_before();
   __syncthreads();
+  // pair: neither CTA leaves or frees TMEM while rank 0's MMAs may still read
+  // its shared memory or write its TMEM (rank 0 drained them)
+  if constexpr (PAIR) cluster_sync();
   tc_fence_after();
-  if (warp == 1) tmem_dealloc(tmem, kTmemCols);
+  if (warp == 1) {
+    if constexpr (PAIR) tmem_dealloc_pair(tmem, kTmemCols);
+    else tmem_dealloc(tmem, kTmemCols);
+  }
+  if (p.tail) grid_dependency_wait();
 }
 
 // ------------------------------------------------------------------ host side
@@ -481,12 +605,44 @@ int make_tmap(CUtensorMap *m, const void *ptr, int64_t k, int64_t rows, int64_t 
   return r == CUDA_SUCCESS ? DG_OK : DG_ERR_CUDA;
 }
 
+// Scale words of `blocks` 128-row blocks: [blocks][ceil(K/128)][128], a box of two
+// K words of `box` row blocks (zeros past K; past the last block, never used).
+int make_scale_tmap(CUtensorMap *m, const void *ptr, int64_t k, int64_t blocks, int box) {
+  EncodeTiledFn enc = encode_tiled_fn();
+  if (!enc) return DG_ERR_CUDA;
+  const cuuint64_t words = static_cast<cuuint64_t>(mx_k_words(k));
+  const cuuint64_t dims[3] = {kMxBlockWords, words, static_cast<cuuint64_t>(blocks)};
+  const cuuint64_t strides[2] = {kMxBlockBytes, kMxBlockBytes * words};
+  const cuuint32_t ext[3] = {kMxBlockWords, kStageWords, static_cast<cuuint32_t>(box)};
+  const cuuint32_t estr[3] = {1, 1, 1};
+  const CUresult r = enc(m, CU_TENSOR_MAP_DATA_TYPE_INT32, 3, const_cast<void *>(ptr), dims,
+                         strides, ext, estr, CU_TENSOR_MAP_INTERLEAVE_NONE,
+                         CU_TENSOR_MAP_SWIZZLE_NONE, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+                         CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
+  return r == CUDA_SUCCESS ? DG_OK : DG_ERR_CUDA;
+}
+
 int ceil_div(int a, int b) { return (a + b - 1) / b; }
 
 constexpr int kMaxDevices = 64;
+// Rows of one launch of the contiguous product (its table of blocks lives in
+// shared memory, eight bytes a block); more rows are several launches.
+constexpr int kMaxContiguousRows = 2048 * 128;
 
-// Most clusters of `size` CTAs (1 .. 8) with all shared memory that are
-// resident at once; asked once per device and size.
+template <int SCHED, bool PAIR>
+int configure(int dev, int smem) {
+  static bool done[kMaxDevices] = {};
+  if (done[dev]) return DG_OK;
+  if (cudaFuncSetAttribute(mxfp4_gemm_kernel<SCHED, PAIR>,
+                           cudaFuncAttributeMaxDynamicSharedMemorySize, smem) != cudaSuccess)
+    return DG_ERR_CUDA;
+  done[dev] = true;
+  return DG_OK;
+}
+
+// Most clusters of `size` CTAs (2 .. 8) with all shared memory that are resident
+// at once; asked once per device, kernel and size.
+template <int SCHED, bool PAIR>
 int clusters_fit(int dev, int size, int smem) {
   static int fit[kMaxDevices][9] = {};  // count + 1; 0 = not asked yet
   if (fit[dev][size] == 0) {
@@ -502,7 +658,7 @@ int clusters_fit(int dev, int size, int smem) {
     q.attrs = a;
     q.numAttrs = 1;
     int n = 0;
-    if (cudaOccupancyMaxActiveClusters(&n, mxfp4_gemm_kernel<kMxDense>, &q) != cudaSuccess) {
+    if (cudaOccupancyMaxActiveClusters(&n, mxfp4_gemm_kernel<SCHED, PAIR>, &q) != cudaSuccess) {
       cudaGetLastError();
       n = 0;
     }
@@ -511,56 +667,33 @@ int clusters_fit(int dev, int size, int smem) {
   return fit[dev][size] - 1;
 }
 
-template <int SCHED>
-int launch_mxfp4(const uint8_t *A, const uint8_t *B, MxParams p, cudaStream_t stream) {
-  const DeviceInfo *info = device_info();
-  int dev = 0;
-  if (!info || cudaGetDevice(&dev) != cudaSuccess || dev < 0 || dev >= kMaxDevices)
-    return DG_ERR_CUDA;
-  const int sms = effective_num_sms();
-  // tokens per tile: the smallest power of two that holds all of them
-  p.tok_tile = 16;
-  while (p.tok_tile < kMaxTokens && p.tok_tile < p.rows) p.tok_tile *= 2;
-  p.tok_tiles = ceil_div(p.rows, p.tok_tile);
-  p.n_tiles = ceil_div(p.n, kTileN);
-  p.splits = 1;
-  const int stage = static_cast<int>(kBBytes) + p.tok_tile * (kStageK / 2) +
+struct Operands {
+  const uint8_t *a, *b;
+  const int32_t *sfa, *sfb;
+};
+
+// Fills in the shapes that follow from p and launches `grid` CTAs.
+template <int SCHED, bool PAIR>
+int launch_form(const Operands &o, MxParams p, int grid, int max_smem, cudaStream_t stream) {
+  const int a_rows = PAIR ? p.tok_tile / 2 : p.tok_tile;
+  const int stage = static_cast<int>(kBBytes) + a_rows * (kStageK / 2) +
                     static_cast<int>(kSfBBytes) * (p.tok_tile > 128 ? 3 : 2);
-  const int tables = SCHED == kMxMasked ? (p.groups + 1) * 4 : 0;
-  const int most = info->max_smem_optin - 2048;  // barriers and alignment
-  p.stages = (most - tables) / stage;
+  const int tables = SCHED == kMxMasked       ? (p.groups + 1) * 4
+                     : SCHED == kMxContiguous ? p.rows / 128 * 8
+                                              : 0;
+  p.stages = (max_smem - 1024 - tables) / stage;
   if (p.stages > kMaxStages) p.stages = kMaxStages;
   int smem = 1024 + p.stages * stage + tables;
   if (smem < kMinSmem) smem = kMinSmem;
-  static bool configured[kMaxDevices] = {};
-  if (!configured[dev]) {
-    if (cudaFuncSetAttribute(mxfp4_gemm_kernel<SCHED>, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                             info->max_smem_optin - 1024) != cudaSuccess)
-      return DG_ERR_CUDA;
-    configured[dev] = true;
-  }
-  int grid = sms;
-  if (SCHED != kMxMasked) {
-    const int tiles = p.tok_tiles * p.n_tiles;
-    if (tiles < grid) grid = tiles;
-    if (SCHED == kMxDense) {
-      // fewer tiles than SMs: split K over the CTAs of a cluster
-      const int k_stages = ceil_div(p.k, kStageK);
-      int s = sms / tiles;
-      if (s > 8) s = 8;
-      if (s > k_stages) s = k_stages;
-      while (s > 1 && clusters_fit(dev, s, info->max_smem_optin - 1024) < tiles) --s;
-      if (s > 1) {
-        p.splits = s;
-        grid = tiles * s;
-      }
-    }
-  }
-  CUtensorMap ta, tb;
+  CUtensorMap ta, tb, tsa, tsb;
   const int slabs = SCHED == kMxMasked ? p.groups : 1;
-  int rc = make_tmap(&ta, A, p.k, p.rows, slabs, p.tok_tile);
-  if (!rc) rc = make_tmap(&tb, B, p.k, p.n, p.groups, kTileN);
+  int rc = make_tmap(&ta, o.a, p.k, p.rows, slabs, a_rows);
+  if (!rc) rc = make_tmap(&tb, o.b, p.k, p.n, p.groups, kTileN);
+  if (!rc) rc = make_scale_tmap(&tsa, o.sfa, p.k, slabs * mx_row_blocks(p.rows),
+                                p.tok_tile > 128 ? 2 : 1);
+  if (!rc) rc = make_scale_tmap(&tsb, o.sfb, p.k, p.groups * mx_row_blocks(p.n), 1);
   if (rc) return rc;
+  const int cluster = PAIR ? 2 : p.splits;
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = dim3(grid);
   cfg.blockDim = dim3(kThreads);
@@ -568,18 +701,78 @@ int launch_mxfp4(const uint8_t *A, const uint8_t *B, MxParams p, cudaStream_t st
   cfg.stream = stream;
   cudaLaunchAttribute attr[2];
   attr[0] = pdl_attribute();
+  attr[1].id = cudaLaunchAttributeClusterDimension;
+  attr[1].val.clusterDim.x = cluster;
+  attr[1].val.clusterDim.y = 1;
+  attr[1].val.clusterDim.z = 1;
   cfg.attrs = attr;
-  cfg.numAttrs = 1;
-  if (p.splits > 1) {
-    attr[1].id = cudaLaunchAttributeClusterDimension;
-    attr[1].val.clusterDim.x = p.splits;
-    attr[1].val.clusterDim.y = 1;
-    attr[1].val.clusterDim.z = 1;
-    cfg.numAttrs = 2;
-  }
-  return cudaLaunchKernelEx(&cfg, mxfp4_gemm_kernel<SCHED>, ta, tb, p) == cudaSuccess
+  cfg.numAttrs = cluster > 1 ? 2 : 1;
+  return cudaLaunchKernelEx(&cfg, mxfp4_gemm_kernel<SCHED, PAIR>, ta, tb, tsa, tsb, p) ==
+                 cudaSuccess
              ? DG_OK
              : DG_ERR_CUDA;
+}
+
+template <int SCHED>
+int launch_mxfp4(const Operands &o, MxParams p, cudaStream_t stream) {
+  const DeviceInfo *info = device_info();
+  int dev = 0;
+  if (!info || cudaGetDevice(&dev) != cudaSuccess || dev < 0 || dev >= kMaxDevices)
+    return DG_ERR_CUDA;
+  const int sms = effective_num_sms();
+  const int max_smem = info->max_smem_optin - 1024;  // (barriers are static)
+  int rc = configure<SCHED, false>(dev, max_smem);
+  if (!rc && SCHED != kMxMasked) rc = configure<SCHED, SCHED != kMxMasked>(dev, max_smem);
+  if (rc) return rc;
+  const int k_stages = ceil_div(p.k, kStageK);
+  // tokens per tile: the smallest power of two that holds all of them
+  p.tok_tile = 16;
+  while (p.tok_tile < kMaxTokens && p.tok_tile < p.rows) p.tok_tile *= 2;
+  p.splits = 1;
+  p.width = 1;
+  if constexpr (SCHED == kMxMasked) {
+    p.n_tiles = ceil_div(p.n, kTileN);
+    return launch_form<SCHED, false>(o, p, sms, max_smem, stream);
+  } else {
+    // pairs that are resident at once
+    int pairs = clusters_fit<SCHED, true>(dev, 2, max_smem);
+    if (pairs > sms / 2) pairs = sms / 2;
+    if constexpr (SCHED == kMxContiguous) {
+      const int most = p.rows / 128;  // blocks that may hold an expert's rows
+      p.n_tiles = ceil_div(p.n, 2 * kTileN);
+      if (pairs > 0 && ceil_div(most, 2) * p.n_tiles >= 2 * pairs) {
+        p.tok_tile = 256;
+        p.width = 2;
+        return launch_form<SCHED, true>(o, p, 2 * pairs, max_smem, stream);
+      }
+      // few tiles: 128 tokens each, for more of them
+      p.tok_tile = 128;
+      p.n_tiles = ceil_div(p.n, kTileN);
+      const int tiles = most * p.n_tiles;
+      return launch_form<SCHED, false>(o, p, tiles < sms ? tiles : sms, max_smem, stream);
+    } else {
+      p.tok_tiles = ceil_div(p.rows, p.tok_tile);
+      p.n_tiles = ceil_div(p.n, 2 * kTileN);
+      p.units = p.tok_tiles * p.n_tiles;
+      if (p.tok_tile == 256 && pairs > 0 && p.units >= pairs) {
+        p.width = 2;
+        return launch_form<SCHED, true>(o, p, 2 * pairs, max_smem, stream);
+      }
+      p.n_tiles = ceil_div(p.n, kTileN);
+      p.units = p.tok_tiles * p.n_tiles;
+      int grid = p.units < sms ? p.units : sms;
+      // fewer tiles than SMs: split K over the CTAs of a cluster
+      int s = sms / p.units;
+      if (s > 8) s = 8;
+      if (s > k_stages) s = k_stages;
+      while (s > 1 && clusters_fit<SCHED, false>(dev, s, max_smem) < p.units) --s;
+      if (s > 1) {
+        p.splits = s;
+        grid = p.units * s;
+      }
+      return launch_form<SCHED, false>(o, p, grid, max_smem, stream);
+    }
+  }
 }
 
 int check_gemm(const void *A, const void *sfa, const void *B, const void *sfb, const void *D,
@@ -604,11 +797,8 @@ int usable_device() {
   return d->ok ? DG_OK : DG_ERR_UNSUPPORTED_ARCH;
 }
 
-MxParams make_params(const int32_t *sfa, const int32_t *sfb, void *D, int64_t rows, int64_t N,
-                     int64_t K, int groups) {
+MxParams make_params(void *D, int64_t rows, int64_t N, int64_t K, int groups) {
   MxParams p{};
-  p.sfa = reinterpret_cast<const uint8_t *>(sfa);
-  p.sfb = reinterpret_cast<const uint8_t *>(sfb);
   p.d = static_cast<uint16_t *>(D);
   p.status = device_info()->status;
   p.rows = static_cast<int>(rows);
@@ -631,7 +821,7 @@ extern "C" int dg_mxfp4_gemm_nt(const uint8_t *A, const int32_t *sfa, const uint
   if (M == 0) return DG_OK;
   rc = usable_device();
   if (rc) return rc;
-  return launch_mxfp4<kMxDense>(A, B, make_params(sfa, sfb, D, M, N, K, 1),
+  return launch_mxfp4<kMxDense>({A, B, sfa, sfb}, make_params(D, M, N, K, 1),
                                 reinterpret_cast<cudaStream_t>(stream));
 }
 
@@ -650,9 +840,17 @@ extern "C" int dg_m_grouped_mxfp4_gemm_nt_contiguous(const uint8_t *A, const int
   if (!aligned16(m_indices)) return DG_ERR_ALIGNMENT;
   rc = usable_device();
   if (rc) return rc;
-  MxParams p = make_params(sfa, sfb, D, M_total, N, K, G);
-  p.m_indices = m_indices;
-  return launch_mxfp4<kMxContiguous>(A, B, p, reinterpret_cast<cudaStream_t>(stream));
+  for (int64_t row = 0; row < M_total; row += kMaxContiguousRows) {
+    const int64_t rows =
+        M_total - row < kMaxContiguousRows ? M_total - row : kMaxContiguousRows;
+    MxParams p = make_params(static_cast<uint16_t *>(D) + row * N, rows, N, K, G);
+    p.m_indices = m_indices + row;
+    rc = launch_mxfp4<kMxContiguous>(
+        {A + row * (K / 2), B, sfa + row / 128 * mx_k_words(K) * kMxBlockWords, sfb}, p,
+        reinterpret_cast<cudaStream_t>(stream));
+    if (rc) return rc;
+  }
+  return DG_OK;
 }
 
 extern "C" int dg_m_grouped_mxfp4_gemm_nt_masked(const uint8_t *A, const int32_t *sfa,
@@ -667,7 +865,7 @@ extern "C" int dg_m_grouped_mxfp4_gemm_nt_masked(const uint8_t *A, const int32_t
   if (reinterpret_cast<uintptr_t>(masked_m) % 4 != 0) return DG_ERR_ALIGNMENT;
   rc = usable_device();
   if (rc) return rc;
-  MxParams p = make_params(sfa, sfb, D, M_max, N, K, G);
+  MxParams p = make_params(D, M_max, N, K, G);
   p.masked_m = masked_m;
-  return launch_mxfp4<kMxMasked>(A, B, p, reinterpret_cast<cudaStream_t>(stream));
+  return launch_mxfp4<kMxMasked>({A, B, sfa, sfb}, p, reinterpret_cast<cudaStream_t>(stream));
 }

@@ -133,7 +133,8 @@ def test_quantize_batch_and_empty():
     (1, 8, 32), (1, 2112, 7168), (2, 136, 96), (5, 128, 128), (16, 256, 288), (17, 1000, 544),
     (33, 264, 1056), (64, 7168, 2048), (100, 264, 160), (128, 256, 512), (129, 512, 1056),
     (255, 384, 800), (256, 128, 64), (257, 1048, 1024), (300, 200, 224), (513, 2112, 736),
-    (1031, 1544, 2080), (40, 24576, 512), (4096, 2112, 512)])
+    (1031, 1544, 2080), (40, 24576, 512), (4096, 2112, 512),
+    (2500, 4104, 544), (1024, 7168, 96)])
 def test_gemm(m, n, k):
     qa, sa, a = operand(rnd((m, k), m + n, outliers=True))
     qb, sb, b = operand(inputs.weights((n, k), k + 1))
@@ -228,7 +229,7 @@ def contiguous(counts, n, k, seed, extra=0):
 @pytest.mark.parametrize("counts,n,k,extra", [
     ([128], 128, 64, 0), ([1, 0, 300], 264, 160, 0), ([256, 256], 384, 512, 0),
     ([130, 0, 0, 5, 700], 1000, 544, 256), ([0, 127, 129, 128], 72, 1056, 128),
-    ([1000, 900], 2112, 736, 0)])
+    ([1000, 900], 2112, 736, 0), ([130, 1, 384, 0, 700, 128, 515], 4872, 288, 128)])
 def test_contiguous(counts, n, k, extra):
     idx, qa, sa, a, qb, sb, b = contiguous(counts, n, k, 11, extra)
     d = sentinel(len(idx), n)
@@ -238,6 +239,25 @@ def test_contiguous(counts, n, k, extra):
         if len(rows):
             check(d[rows], a[rows], b[e], f"expert {e}")
     assert untouched(d[torch.from_numpy(idx < 0).cuda()])
+    assert dg.dg_get_device_status() == 0
+
+
+def test_contiguous_many_rows():
+    """More 128-row blocks than one launch's table holds, every expert's run cut."""
+    rows, n, k, g = 262144 + 640, 16, 32, 3
+    idx = torch.arange(rows, device="cuda", dtype=torch.int32) // 128 % (g + 1)
+    idx = torch.where(idx == g, -1, idx)
+    idx[-384:] = 1
+    gen = torch.Generator(device="cuda").manual_seed(3)
+    q = torch.randint(0, 256, (rows, k // 2), generator=gen, device="cuda", dtype=torch.uint8)
+    qb, sb, b = operand(inputs.weights((g, n, k), 4))
+    sf = torch.full((rows // 128, 1, 32, 4), 0x7F, device="cuda", dtype=torch.int32)
+    a = dev(mxfp4.VALUES)[torch.stack([q & 15, q >> 4], -1).flatten(1).long()]
+    d = sentinel(rows, n)
+    dg.dg_m_grouped_mxfp4_gemm_nt_contiguous(q, sf, qb, sb, d, idx)
+    for e in range(g):
+        check(d[idx == e], a[idx == e], b[e], f"expert {e}")
+    assert untouched(d[idx < 0])
     assert dg.dg_get_device_status() == 0
 
 
