@@ -50,6 +50,9 @@ constexpr int kSfSlots = 4;
 // for TMEM there while its peers wait for it could deadlock two launches).
 constexpr int kMinSmem = 120 * 1024;
 
+// A dense launch of several waves may leave its last tiles to a second launch.
+enum Tail : int { kAlone = 0, kHasTail = 1, kIsTail = 2 };
+
 struct MxParams {
   uint16_t *d;
   const int32_t *m_indices, *masked_m;
@@ -64,7 +67,7 @@ struct MxParams {
   int unit0, units;  // dense: the units (tiles, or pairs of them) of this launch
   int stages;
   int splits;        // CTAs of a cluster that split a tile's K (dense; 1: none)
-  int tail;          // dense: this launch is the tail of another (see launch_mxfp4)
+  int tail;          // dense: kAlone, kHasTail or kIsTail (see launch_mxfp4)
 };
 
 struct Tile {
@@ -225,6 +228,7 @@ mxfp4_gemm_kernel(const __grid_constant__ CUtensorMap tmap_a,
   tab.list = s_table + blocks;
   tab.count = 0;
 
+  if (p.tail != kHasTail) grid_launch_dependents();
   if (SCHED == kMxDense && warp == 3) {
     // B's boxes of the first stages are asked into L2 before the set-up and the
     // dependency wait (a prefetch only fills L2, which the previous kernel's
@@ -262,11 +266,12 @@ mxfp4_gemm_kernel(const __grid_constant__ CUtensorMap tmap_a,
       tmem_relinquish();
     }
   }
-  // A tail does not read what the launch before it writes, and that launch let
-  // it start only after the kernels before both had completed; it waits for it
-  // at its own end instead, so that whatever follows the tail follows both.
-  if (!p.tail) grid_dependency_wait();
-  grid_launch_dependents();
+  // A tail does not read what the launch before it writes, so it does not wait
+  // for it here: that launch lets it start only once the kernels before both
+  // have completed.  It waits at its own end instead, so that whatever follows
+  // the tail follows both.
+  if (p.tail != kIsTail) grid_dependency_wait();
+  if (p.tail == kHasTail) grid_launch_dependents();
   if constexpr (SCHED == kMxMasked) {
     if (warp == 2) {
       int running = 0;
@@ -582,7 +587,7 @@ mxfp4_gemm_kernel(const __grid_constant__ CUtensorMap tmap_a,
     if constexpr (PAIR) tmem_dealloc_pair(tmem, kTmemCols);
     else tmem_dealloc(tmem, kTmemCols);
   }
-  if (p.tail) grid_dependency_wait();
+  if (p.tail == kIsTail) grid_dependency_wait();
 }
 
 // ------------------------------------------------------------------ host side
@@ -665,6 +670,16 @@ int clusters_fit(int dev, int size, int smem) {
     fit[dev][size] = n + 1;
   }
   return fit[dev][size] - 1;
+}
+
+// CTAs of a cluster that split K, at most `most`, for `tiles` tiles of one wave.
+template <int SCHED>
+int pick_splits(int dev, int tiles, int k_stages, int sms, int most, int smem) {
+  int s = sms / tiles;
+  if (s > most) s = most;
+  if (s > k_stages) s = k_stages;
+  while (s > 1 && clusters_fit<SCHED, false>(dev, s, smem) < tiles) --s;
+  return s;
 }
 
 struct Operands {
@@ -754,23 +769,41 @@ int launch_mxfp4(const Operands &o, MxParams p, cudaStream_t stream) {
       p.tok_tiles = ceil_div(p.rows, p.tok_tile);
       p.n_tiles = ceil_div(p.n, 2 * kTileN);
       p.units = p.tok_tiles * p.n_tiles;
-      if (p.tok_tile == 256 && pairs > 0 && p.units >= pairs) {
+      const bool pair = p.tok_tile == 256 && pairs > 0 && p.units >= pairs;
+      if (pair) {
         p.width = 2;
-        return launch_form<SCHED, true>(o, p, 2 * pairs, max_smem, stream);
+      } else {
+        p.n_tiles = ceil_div(p.n, kTileN);
+        p.units = p.tok_tiles * p.n_tiles;
+        // fewer tiles than SMs: split K over the CTAs of a cluster
+        p.splits = p.units < sms
+                       ? pick_splits<SCHED>(dev, p.units, k_stages, sms, 8, max_smem)
+                       : 1;
+        if (p.splits > 1) return launch_form<SCHED, false>(o, p, p.units * p.splits, max_smem, stream);
       }
-      p.n_tiles = ceil_div(p.n, kTileN);
-      p.units = p.tok_tiles * p.n_tiles;
-      int grid = p.units < sms ? p.units : sms;
-      // fewer tiles than SMs: split K over the CTAs of a cluster
-      int s = sms / p.units;
-      if (s > 8) s = 8;
-      if (s > k_stages) s = k_stages;
-      while (s > 1 && clusters_fit<SCHED, false>(dev, s, max_smem) < p.units) --s;
-      if (s > 1) {
-        p.splits = s;
-        grid = p.units * s;
+      // Whole waves, then the rest split along K in a second launch that fills
+      // the SMs as they come free: a last wave of few tiles takes 1/S of a
+      // wave instead of a whole one.  A split costs about as much as kTailCost
+      // stages (the cluster's reduction), so short K keeps the whole wave.
+      constexpr int kTailCost = 10;
+      const int wave = pair ? pairs : sms;
+      const int rest = p.units % wave;
+      MxParams t = p;
+      if (p.units > wave && rest > 0) {
+        t.splits = pick_splits<SCHED>(dev, rest * p.width, k_stages, sms, 8, max_smem);
+        if (t.splits > 1 && k_stages - k_stages / t.splits >= kTailCost) {
+          t.tail = kIsTail;
+          t.unit0 = p.units - rest;
+          t.units = rest;
+          p.tail = kHasTail;
+          p.units -= rest;
+        }
       }
-      return launch_form<SCHED, false>(o, p, grid, max_smem, stream);
+      const int grid = p.units < wave ? p.units : wave;
+      rc = pair ? launch_form<SCHED, true>(o, p, 2 * grid, max_smem, stream)
+                : launch_form<SCHED, false>(o, p, grid, max_smem, stream);
+      if (rc || p.tail == kAlone) return rc;
+      return launch_form<SCHED, false>(o, t, rest * t.width * t.splits, max_smem, stream);
     }
   }
 }
