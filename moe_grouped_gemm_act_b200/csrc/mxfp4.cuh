@@ -126,6 +126,28 @@ __device__ __forceinline__ void umma_mxf4(uint32_t d_tmem, uint64_t a_desc, uint
       : "memory");
 }
 
+// TMEM -> registers, 16 lanes x 16 columns of 32 bits: thread t gets, of column
+// block b (8 columns), r[4b], r[4b+1] = lane t/4, columns 2 (t%4), +1, and
+// r[4b+2], r[4b+3] the same of lane t/4 + 8 -- the fragments of 8 x 8 matrices
+// that stmatrix takes.
+__device__ __forceinline__ void tmem_ld_16x256_x2(uint32_t taddr, uint32_t *r) {
+  asm volatile(
+      "tcgen05.ld.sync.aligned.16x256b.x2.b32 {%0, %1, %2, %3, %4, %5, %6, %7}, [%8];"
+      : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]),
+        "=r"(r[7])
+      : "r"(taddr));
+}
+
+// Four 8 x 8 matrices of 16-bit elements, transposed, to shared memory: thread
+// 8m + i gives the address of the 16 bytes that hold column i of matrix m.
+__device__ __forceinline__ void stmatrix_x4_trans(uint32_t addr, uint32_t a, uint32_t b,
+                                                  uint32_t c, uint32_t d) {
+  asm volatile("stmatrix.sync.aligned.m8n8.x4.trans.shared.b16 [%0], {%1, %2, %3, %4};" ::"r"(
+                   addr),
+               "r"(a), "r"(b), "r"(c), "r"(d)
+               : "memory");
+}
+
 // The CTA-pair form: M = 256, rows 0-127 of A, of D and A's scales in rank 0,
 // rows 128-255 in rank 1; B split along N between the two CTAs' shared memory,
 // its scales whole in both CTAs' TMEM.  Issued by one thread of rank 0.

@@ -36,6 +36,7 @@ constexpr int kStageWords = kStageK / 128;
 constexpr int kThreads = 384;    // producer, MMA, two set-up warps, 8 epilogue warps
 constexpr int kEpiWarps = 8;
 constexpr int kFirstEpiWarp = 4;
+constexpr int kTurnBytes = 1024;  // per epilogue warp: 16 tokens x 32 columns of D
 constexpr int kMaxStages = 12;
 constexpr uint32_t kBBytes = kTileN * kStageK / 2;              // 16 KB
 constexpr uint32_t kSfBBytes = kStageWords * kMxBlockBytes;     // one row block
@@ -208,6 +209,7 @@ mxfp4_gemm_kernel(const __grid_constant__ CUtensorMap tmap_a,
   const uint32_t sf_base = base + static_cast<uint32_t>(p.stages) * stage_bytes;
   int *s_table = reinterpret_cast<int *>(
       smem_raw + (sf_base - raw) + static_cast<uint32_t>(p.stages) * sf_stage);
+  __shared__ __align__(16) uint8_t s_turn[kEpiWarps * kTurnBytes];
   const uint32_t bars = smem_u32(s_bars);
   auto full_bar = [&](int s) { return bars + 8u * s; };
   auto empty_bar = [&](int s) { return bars + 8u * (kMaxStages + s); };
@@ -450,9 +452,11 @@ mxfp4_gemm_kernel(const __grid_constant__ CUtensorMap tmap_a,
   } else if (warp >= kFirstEpiWarp) {
     // ================================================================ epilogue
     // Warp w reads lanes 32 (w mod 4) .. and every other 16-column chunk; the
-    // accumulator is handed back once it is in registers, as BF16.
+    // accumulator is handed back once it is in registers, as BF16 (a tile of 256
+    // tokens has the only accumulator, so the MMAs of the next one wait).
     const int half = (warp - kFirstEpiWarp) >> 2;
     const int quarter = warp & 3;
+    const uint32_t turn = smem_u32(s_turn) + (warp - kFirstEpiWarp) * kTurnBytes;
     int tile_i = 0;
     for_each_tile<SCHED, PAIR>(p, tab, [&](const Tile &t) {
       const int buf = tile_i % nbuf;
@@ -493,20 +497,29 @@ mxfp4_gemm_kernel(const __grid_constant__ CUtensorMap tmap_a,
         ++tile_i;
         return true;
       }
+      // out[i]: 16 tokens of the warp's 32 columns, as 8 x 8 matrices: [4 h + m],
+      // h the 16-lane half, m = 2 (token / 8) + (column / 8) within it
       uint32_t out[8][8];
 #pragma unroll
-      for (int i = 0; i < 8; ++i) {
-        const int c0 = (2 * i + half) * 16;
-        if (c0 < t.tokens) {
-          uint32_t r[16];
-          tmem_ld<16>(acc + c0, r);
-          tmem_wait_ld();
-          reg_barrier<16>(r);
+      for (int i = 0; i < 8; i += 2) {
+        uint32_t r[2][16];
+#pragma unroll
+        for (int q = 0; q < 2; ++q) {
+          const int c0 = (2 * (i + q) + half) * 16;
+          if (c0 < t.tokens) {
+            tmem_ld_16x256_x2(acc + c0, r[q]);
+            tmem_ld_16x256_x2(acc + c0 + (16u << 16), r[q] + 8);
+          }
+        }
+        tmem_wait_ld();
+#pragma unroll
+        for (int q = 0; q < 2; ++q) {
+          reg_barrier<16>(r[q]);
 #pragma unroll
           for (int j = 0; j < 8; ++j) {
-            const __nv_bfloat162 v = __floats2bfloat162_rn(__uint_as_float(r[2 * j]),
-                                                           __uint_as_float(r[2 * j + 1]));
-            out[i][j] = *reinterpret_cast<const uint32_t *>(&v);
+            const __nv_bfloat162 v = __floats2bfloat162_rn(__uint_as_float(r[q][2 * j]),
+                                                           __uint_as_float(r[q][2 * j + 1]));
+            out[i + q][j] = *reinterpret_cast<const uint32_t *>(&v);
           }
         }
       }
@@ -516,26 +529,33 @@ mxfp4_gemm_kernel(const __grid_constant__ CUtensorMap tmap_a,
         if constexpr (PAIR) mbar_arrive_cluster(mapa_shared(tempty_bar(buf), 0));
         else mbar_arrive(tempty_bar(buf));
       }
-      // neighbouring lanes hold neighbouring columns of D: each pair of lanes
-      // swaps halves so that the even lane stores two columns of one token,
-      // the odd lane of the next (a warp's store: 64 bytes of two rows)
-      const int odd = lane & 1;
-      const int n = t.n0 + quarter * 32 + (lane & ~1);
-      uint16_t *dst = p.d + (static_cast<int64_t>(t.slab) * p.rows + t.tok0) * p.n + n;
+      // Turned to [token][column] in the warp's own kilobyte of shared memory (16
+      // tokens of 64 bytes; 16-byte piece c of token t at c ^ (t / 2 mod 4):
+      // no bank conflicts), then stored as 64 bytes of eight rows at a time.
+      const uint32_t st_tok = (lane & 7) + 8 * (lane >> 4);
+      const uint32_t st_piece = (lane >> 3) & 1;
+      const uint32_t st_row = turn + st_tok * 64;
+      const uint32_t st_a = st_row + ((st_piece ^ ((st_tok >> 1) & 3)) << 4);
+      const uint32_t st_b = st_row + (((st_piece + 2) ^ ((st_tok >> 1) & 3)) << 4);
+      const int tok = lane >> 2;
+      const uint32_t ld = turn + tok * 64 + (((lane & 3) ^ ((tok >> 1) & 3)) << 4);
+      const int n = t.n0 + quarter * 32 + 8 * (lane & 3);
+      uint16_t *dst = p.d + (static_cast<int64_t>(t.slab) * p.rows + t.tok0 + tok) * p.n + n;
 #pragma unroll
       for (int i = 0; i < 8; ++i) {
         const int c0 = (2 * i + half) * 16;
         if (c0 < t.tokens) {
-          const uint32_t bits = live[i] >> (16 * half + odd);
-#pragma unroll
-          for (int j = 0; j < 8; ++j) {
-            const uint32_t other = __shfl_xor_sync(0xffffffffu, out[i][j], 1);
-            const uint32_t v = odd ? __byte_perm(other, out[i][j], 0x7632)
-                                   : __byte_perm(out[i][j], other, 0x5410);
-            if (((bits >> (2 * j)) & 1u) && n < p.n)
-              *reinterpret_cast<uint32_t *>(dst + static_cast<int64_t>(c0 + 2 * j + odd) * p.n) =
-                  v;
+          stmatrix_x4_trans(st_a, out[i][0], out[i][1], out[i][2], out[i][3]);
+          stmatrix_x4_trans(st_b, out[i][4], out[i][5], out[i][6], out[i][7]);
+          __syncwarp();
+          const uint4 v0 = ld_shared_v4(ld), v1 = ld_shared_v4(ld + 512);
+          const uint32_t bits = live[i] >> (16 * half + tok);
+          uint16_t *row = dst + static_cast<int64_t>(c0) * p.n;
+          if (n < p.n) {  // (N % 8 == 0: eight columns or none)
+            if (bits & 1u) *reinterpret_cast<uint4 *>(row) = v0;
+            if (bits & 256u) *reinterpret_cast<uint4 *>(row + static_cast<int64_t>(8) * p.n) = v1;
           }
+          __syncwarp();
         }
       }
       ++tile_i;
@@ -735,7 +755,8 @@ int launch_mxfp4(const Operands &o, MxParams p, cudaStream_t stream) {
   if (!info || cudaGetDevice(&dev) != cudaSuccess || dev < 0 || dev >= kMaxDevices)
     return DG_ERR_CUDA;
   const int sms = effective_num_sms();
-  const int max_smem = info->max_smem_optin - 1024;  // (barriers are static)
+  // (the barriers and the epilogue's turning area are static)
+  const int max_smem = info->max_smem_optin - kEpiWarps * kTurnBytes - 512;
   int rc = configure<SCHED, false>(dev, max_smem);
   if (!rc && SCHED != kMxMasked) rc = configure<SCHED, SCHED != kMxMasked>(dev, max_smem);
   if (rc) return rc;
