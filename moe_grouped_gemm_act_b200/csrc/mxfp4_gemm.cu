@@ -178,6 +178,20 @@ __device__ __forceinline__ void for_each_tile(const MxParams &p, const Tables &t
   }
 }
 
+// A role's place in the stage ring: the slot, and the parity of its use there.
+// (Carried along: a division per stage by the run-time number of stages cost
+// each role about a hundred cycles.)
+struct Ring {
+  int slot = 0;
+  uint32_t parity = 0;
+  __device__ __forceinline__ void advance(int stages) {
+    if (++slot == stages) {
+      slot = 0;
+      parity ^= 1;
+    }
+  }
+};
+
 // Rows of A (MMA columns) of a tile: a multiple of 16, of 32 for the pair,
 // whose CTAs hold half of them each.
 template <bool PAIR>
@@ -344,14 +358,15 @@ mxfp4_gemm_kernel(const __grid_constant__ CUtensorMap tmap_a,
 
   if (warp == 0) {
     // ================================================================ producer
-    int it = 0;
+    Ring ring;
+    int issued = 0;  // stages, counted up to the ring's length
     for_each_tile<SCHED, PAIR>(p, tab, [&](const Tile &t) {
       const int b_block = t.group * b_blocks + t.n0 / 128;
       const int a_block = t.slab * a_blocks + t.tok0 / 128;
       const int a_row = t.tok0 + static_cast<int>(rank) * (mma_n<PAIR>(t) / 2);
-      for (int ks = t.k_begin; ks < t.k_end; ++ks, ++it) {
-        const int s = it % p.stages;
-        if (!mbar_wait(empty_bar(s), ((it / p.stages) & 1) ^ 1, abort, p.status)) return false;
+      for (int ks = t.k_begin; ks < t.k_end; ++ks) {
+        const int s = ring.slot;
+        if (!mbar_wait(empty_bar(s), ring.parity ^ 1, abort, p.status)) return false;
         if (elect_one()) {
           const uint32_t sb = base + static_cast<uint32_t>(s) * stage_bytes;
           const uint32_t sf = sf_base + static_cast<uint32_t>(s) * sf_stage;
@@ -373,59 +388,79 @@ mxfp4_gemm_kernel(const __grid_constant__ CUtensorMap tmap_a,
           }
         }
         __syncwarp();
+        ring.advance(p.stages);
+        if (issued < p.stages) ++issued;
       }
       return true;
     });
-    // no copy may still be writing this CTA's shared memory when it exits
-    // (pair: rank 0's barriers count both CTAs' bytes, and rank 1 leaves after
-    // rank 0 at the cluster barrier)
+    // no copy may still be writing this CTA's shared memory when it exits: wait
+    // for the last use of every stage that was armed (pair: rank 0's barriers
+    // count both CTAs' bytes, and rank 1 leaves after rank 0 at the cluster
+    // barrier)
     volatile int never = 0;
     if (rank == 0)
-      for (int i = max(0, it - p.stages); i < it; ++i)
-        mbar_wait(full_bar(i % p.stages), (i / p.stages) & 1, &never, p.status);
+      for (int i = 0; i < issued; ++i) {
+        // slots before the ring's place were used with its parity, the others
+        // with the one before
+        mbar_wait(full_bar(i), i < ring.slot ? ring.parity : ring.parity ^ 1, &never, p.status);
+      }
   } else if (warp == 1) {
     // ================================================================ MMA issuer
     if (rank == 0) {
       const int k_mmas = (p.k + kMmaK - 1) / kMmaK;
-      int it = 0, tile_i = 0;
+      const uint64_t bdesc0 = smem_desc_k128_sw128(base);
+      const uint64_t sfdesc0 = smem_desc_rows16(sf_base);
+      Ring ring;
+      uint32_t it = 0;
+      int tile_i = 0;
       for_each_tile<SCHED, PAIR>(p, tab, [&](const Tile &t) {
-        const int buf = tile_i % nbuf;
-        if (!mbar_wait(tempty_bar(buf), ((tile_i / nbuf) & 1) ^ 1, abort, p.status)) return false;
+        const int buf = nbuf == 2 ? tile_i & 1 : 0;
+        const uint32_t use = nbuf == 2 ? tile_i >> 1 : tile_i;
+        if (!mbar_wait(tempty_bar(buf), (use & 1) ^ 1, abort, p.status)) return false;
         const uint32_t d = tmem + static_cast<uint32_t>(buf) * buf_cols;
         const uint32_t idesc = idesc_mxf4(PAIR ? 2 * kTileN : kTileN, mma_n<PAIR>(t));
+        const bool second = t.tokens > 128;
         for (int ks = t.k_begin; ks < t.k_end; ++ks, ++it) {
-          const int s = it % p.stages;
-          if (!mbar_wait(full_bar(s), (it / p.stages) & 1, abort, p.status)) return false;
+          const int s = ring.slot;
+          if (!mbar_wait(full_bar(s), ring.parity, abort, p.status)) return false;
           tc_fence_after();
           if (elect_one()) {
-            const uint32_t sb = base + static_cast<uint32_t>(s) * stage_bytes;
-            const uint32_t sf = sf_base + static_cast<uint32_t>(s) * sf_stage;
-            const uint32_t slot =
-                tmem + kSfCol + static_cast<uint32_t>(it % kSfSlots) * kSfSlotCols;
+            // (descriptor addresses are in units of 16 bytes, below 2^14: no carry)
+            const uint64_t bdesc = bdesc0 + static_cast<uint32_t>(s) * (stage_bytes >> 4);
+            const uint64_t adesc = bdesc + (kBBytes >> 4);
+            const uint64_t sfdesc = sfdesc0 + static_cast<uint32_t>(s) * (sf_stage >> 4);
+            const uint32_t slot = tmem + kSfCol + (it % kSfSlots) * kSfSlotCols;
+            const uint32_t first = ks == t.k_begin ? 1u : 0u;
             auto cp = [&](uint32_t to, uint32_t from) {
-              if constexpr (PAIR) tmem_cp_32x128b_x4_pair(to, smem_desc_rows16(from));
-              else tmem_cp_32x128b_x4(to, smem_desc_rows16(from));
+              if constexpr (PAIR) tmem_cp_32x128b_x4_pair(slot + to, sfdesc + (from >> 4));
+              else tmem_cp_32x128b_x4(slot + to, sfdesc + (from >> 4));
             };
-            const int words = min(kStageWords, k_words - ks * kStageWords);
-            for (int w = 0; w < words; ++w) {
-              cp(slot + 4 * w, sf + kMxBlockBytes * w);
-              cp(slot + 8 + 8 * w, sf + kSfBBytes + kMxBlockBytes * w);
-              if (t.tokens > 128) cp(slot + 12 + 8 * w, sf + 2 * kSfBBytes + kMxBlockBytes * w);
-            }
-            const uint64_t bdesc = smem_desc_k128_sw128(sb);
-            const uint64_t adesc = smem_desc_k128_sw128(sb + kBBytes);
-            const int mmas = min(kStageK / kMmaK, k_mmas - ks * (kStageK / kMmaK));
+            auto scales = [&](int w) {
+              cp(4 * w, kMxBlockBytes * w);
+              cp(8 + 8 * w, kSfBBytes + kMxBlockBytes * w);
+              if (second) cp(12 + 8 * w, 2 * kSfBBytes + kMxBlockBytes * w);
+            };
+            auto mma = [&](int j) {
+              const uint32_t sfb = slot + 4 * (j >> 1), sfa = slot + 8 + 8 * (j >> 1);
+              const uint32_t more = j > 0 ? 1u : first ^ 1u;
+              if constexpr (PAIR)
+                umma_mxf4_pair(d, bdesc + 2 * j, adesc + 2 * j, idesc, sfb, sfa, 2u * (j & 1),
+                               more);
+              else
+                umma_mxf4(d, bdesc + 2 * j, adesc + 2 * j, idesc, sfb, sfa, 2u * (j & 1), more);
+            };
+            const int mmas = k_mmas - ks * (kStageK / kMmaK);
+            scales(0);
+            if (mmas >= kStageK / kMmaK) {
+              scales(1);
 #pragma unroll
-            for (int j = 0; j < kStageK / kMmaK; ++j) {
-              if (j < mmas) {
-                const uint32_t more = ks > t.k_begin || j > 0 ? 1u : 0u;
-                const uint32_t sfb = slot + 4 * (j >> 1), sfa = slot + 8 + 8 * (j >> 1);
-                if constexpr (PAIR)
-                  umma_mxf4_pair(d, bdesc + 2 * j, adesc + 2 * j, idesc, sfb, sfa, 2u * (j & 1),
-                                 more);
-                else
-                  umma_mxf4(d, bdesc + 2 * j, adesc + 2 * j, idesc, sfb, sfa, 2u * (j & 1), more);
-              }
+              for (int j = 0; j < kStageK / kMmaK; ++j) mma(j);
+            } else {
+              // the last stage of a K off the 256 grid
+              if (mmas > 2) scales(1);
+              mma(0);
+              if (mmas > 1) mma(1);
+              if (mmas > 2) mma(2);
             }
             if constexpr (PAIR) {
               umma_commit_pair_both(empty_bar(s));
@@ -436,6 +471,7 @@ mxfp4_gemm_kernel(const __grid_constant__ CUtensorMap tmap_a,
             }
           }
           __syncwarp();
+          ring.advance(p.stages);
         }
         ++tile_i;
         return true;
@@ -459,7 +495,8 @@ mxfp4_gemm_kernel(const __grid_constant__ CUtensorMap tmap_a,
     const uint32_t turn = smem_u32(s_turn) + (warp - kFirstEpiWarp) * kTurnBytes;
     int tile_i = 0;
     for_each_tile<SCHED, PAIR>(p, tab, [&](const Tile &t) {
-      const int buf = tile_i % nbuf;
+      const int buf = nbuf == 2 ? tile_i & 1 : 0;
+      const uint32_t use = nbuf == 2 ? tile_i >> 1 : tile_i;
       // rows that are stored: bit l of live[i] is token 32 i + l
       uint32_t live[8];
       bool mixed = false;
@@ -474,7 +511,7 @@ mxfp4_gemm_kernel(const __grid_constant__ CUtensorMap tmap_a,
         live[i] = __ballot_sync(0xffffffffu, v);
       }
       if (SCHED == kMxContiguous && mixed) record_status(p.status, DG_ERR_DEVICE_DATA);
-      if (!mbar_wait(tfull_bar(buf), (tile_i / nbuf) & 1, abort, p.status)) return false;
+      if (!mbar_wait(tfull_bar(buf), use & 1, abort, p.status)) return false;
       tc_fence_after();
       const uint32_t acc = tmem + static_cast<uint32_t>(buf) * buf_cols +
                            (static_cast<uint32_t>(quarter * 32) << 16);
