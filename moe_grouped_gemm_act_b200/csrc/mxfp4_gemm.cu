@@ -78,28 +78,25 @@ struct Tile {
   int k_begin, k_end;  // stages
 };
 
-// Contiguous layout: the expert of a 128-row block, its first non-negative
-// index, -1 when it is all padding or the index is out of range.  One thread;
-// the first row answers for a block that has any expert at all in nearly every
-// layout.
-__device__ __forceinline__ int block_expert(const MxParams &p, int block) {
-  int e = __ldg(p.m_indices + static_cast<int64_t>(block) * 128);
-  if (e < 0) {
-    const int4 *v = reinterpret_cast<const int4 *>(p.m_indices) + static_cast<int64_t>(block) * 32;
-    for (int i = 0; i < 32 && e < 0; i += 8) {
-      int4 w[8];
+// Contiguous layout: the expert of a 128-row block from its 128 indices, four per
+// lane: the first non-negative one, -1 when the block is all padding or that
+// index is out of range.  A block that mixes experts or names one out of range
+// records DG_ERR_DEVICE_DATA (only the rows of the first expert are computed).
+// Whole warp.
+__device__ __forceinline__ int block_expert(const MxParams &p, const int4 &v) {
+  const int vals[4] = {v.x, v.y, v.z, v.w};
+  int first = -1;
 #pragma unroll
-      for (int j = 0; j < 8; ++j) w[j] = __ldg(v + i + j);
+  for (int i = 3; i >= 0; --i)
+    if (vals[i] >= 0) first = vals[i];
+  const unsigned any = __ballot_sync(0xffffffffu, first >= 0);
+  if (!any) return -1;
+  const int e = __shfl_sync(0xffffffffu, first, __ffs(any) - 1);
+  bool bad = e >= p.groups;
 #pragma unroll
-      for (int j = 7; j >= 0; --j) {
-        if (w[j].w >= 0) e = w[j].w;
-        if (w[j].z >= 0) e = w[j].z;
-        if (w[j].y >= 0) e = w[j].y;
-        if (w[j].x >= 0) e = w[j].x;
-      }
-    }
-  }
-  return e;
+  for (int i = 0; i < 4; ++i) bad |= vals[i] >= 0 && vals[i] != e;
+  if (bad) record_status(p.status, DG_ERR_DEVICE_DATA);
+  return e < p.groups ? e : -1;
 }
 
 // What a launch's roles read about its tiles, in shared memory.  Masked:
@@ -311,13 +308,24 @@ mxfp4_gemm_kernel(const __grid_constant__ CUtensorMap tmap_a,
     }
   }
   if constexpr (SCHED == kMxContiguous) {
-    for (int b = threadIdx.x; b < blocks; b += kThreads) {
-      int e = block_expert(p, b);
-      if (e >= p.groups) {
-        record_status(p.status, DG_ERR_DEVICE_DATA);
-        e = -1;
+    // (one round trip for four blocks of each warp)
+    constexpr int kWarps = kThreads / 32, kAtOnce = 4;
+    const int4 *idx = reinterpret_cast<const int4 *>(p.m_indices);
+    for (int b0 = warp; b0 < blocks; b0 += kWarps * kAtOnce) {
+      int4 v[kAtOnce];
+#pragma unroll
+      for (int j = 0; j < kAtOnce; ++j) {
+        const int b = b0 + j * kWarps;
+        if (b < blocks) v[j] = __ldg(idx + static_cast<int64_t>(b) * 32 + lane);
       }
-      s_table[b] = e;
+#pragma unroll
+      for (int j = 0; j < kAtOnce; ++j) {
+        const int b = b0 + j * kWarps;
+        if (b < blocks) {
+          const int e = block_expert(p, v[j]);
+          if (lane == 0) s_table[b] = e;
+        }
+      }
     }
     __syncthreads();
     if (warp == 2) {
@@ -357,8 +365,8 @@ mxfp4_gemm_kernel(const __grid_constant__ CUtensorMap tmap_a,
 
   if (warp == 0) {
     // ================================================================ producer
-    // (one elected thread runs the role, and one the MMA issuer's: waiting with
-    // the whole warp and electing per stage took 0.24 us a stage against 0.21)
+    // (one elected thread runs the role, and one the MMA issuer's: 0.21 us a stage
+    // of a small tile; waiting with the whole warp and electing per stage, 0.24)
     if (elect_one()) {
     Ring ring;
     int issued = 0;  // stages, counted up to the ring's length
@@ -501,18 +509,13 @@ mxfp4_gemm_kernel(const __grid_constant__ CUtensorMap tmap_a,
       const uint32_t use = nbuf == 2 ? tile_i >> 1 : tile_i;
       // rows that are stored: bit l of live[i] is token 32 i + l
       uint32_t live[8];
-      bool mixed = false;
 #pragma unroll
       for (int i = 0; i < 8; ++i) {
         bool v = 32 * i + lane < t.tokens;
-        if (SCHED == kMxContiguous && v) {
-          const int e = __ldg(p.m_indices + t.tok0 + 32 * i + lane);
-          v = e == t.group;
-          mixed |= !v && e >= 0;
-        }
+        if (SCHED == kMxContiguous && v)
+          v = __ldg(p.m_indices + t.tok0 + 32 * i + lane) == t.group;
         live[i] = __ballot_sync(0xffffffffu, v);
       }
-      if (SCHED == kMxContiguous && mixed) record_status(p.status, DG_ERR_DEVICE_DATA);
       if (!mbar_wait(tfull_bar(buf), use & 1, abort, p.status)) return false;
       tc_fence_after();
       const uint32_t acc = tmem + static_cast<uint32_t>(buf) * buf_cols +
