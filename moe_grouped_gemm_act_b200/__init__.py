@@ -696,14 +696,15 @@ def _exact(t, name, dtype, shape):
         raise ValueError("tensors must be contiguous")
 
 
-def _empty(shape, dtype, device, stream):
-    """An uninitialised tensor for a call on `stream`: it comes from that stream's
-    memory pool, so that nothing still running on the current stream holds it, and
-    is marked as used on the current stream, where the caller gets it."""
+def _empty(like, shape, dtype, stream):
+    """An uninitialised tensor on like's device for a call on `stream`: it comes
+    from that stream's memory pool, so that nothing still running on the current
+    stream holds it, and is marked as used on the current stream, where the
+    caller gets it."""
     if stream is None:
-        return torch.empty(shape, dtype=dtype, device=device)
+        return like.new_empty(shape, dtype=dtype)
     with torch.cuda.stream(stream):
-        t = torch.empty(shape, dtype=dtype, device=device)
+        t = like.new_empty(shape, dtype=dtype)
     t.record_stream(torch.cuda.current_stream(t.device))
     return t
 
@@ -752,9 +753,9 @@ def dg_quantize_mxfp4(x: torch.Tensor, transpose: bool = False, q=None, sf=None,
     if lead == (0,):
         raise ValueError("an empty batch")
     if q is None:
-        q = _empty(lead + (m, k // 2), torch.uint8, x.device, stream)
+        q = _empty(x, lead + (m, k // 2), torch.uint8, stream)
     if sf is None:
-        sf = _empty(lead + _mx_scales(m, k), torch.int32, x.device, stream)
+        sf = _empty(x, lead + _mx_scales(m, k), torch.int32, stream)
     _exact(q, "q", torch.uint8, lead + (m, k // 2))
     _exact(sf, "sf", torch.int32, lead + _mx_scales(m, k))
     _on_device("dg_quantize_mxfp4",
@@ -780,7 +781,7 @@ def dg_dequantize_mxfp4(q: torch.Tensor, sf: torch.Tensor, dtype: torch.dtype = 
     if lead == (0,):
         raise ValueError("an empty batch")
     if out is None:
-        out = _empty(lead + (m, k), dtype, q.device, stream)
+        out = _empty(q, lead + (m, k), dtype, stream)
     _exact(q, "q", torch.uint8, lead + (m, kh))
     _exact(sf, "sf", torch.int32, lead + _mx_scales(m, k))
     _exact(out, "out", dtype, lead + (m, k))
@@ -875,17 +876,17 @@ def dg_moe_route(logits: torch.Tensor, top_k: int, normalize: bool = True, token
         raise ValueError(f"top_k = {top_k} must be in 1 .. min(E, 32), E = {e}")
     if not logits.is_cuda:
         raise ValueError("all tensors must be CUDA tensors (there is no CPU path)")
-    idx = _empty((t, top_k), torch.int32, dev, stream)
-    weights = _empty((t, top_k), torch.float32, dev, stream)
-    counts = _empty((e,), torch.int32, dev, stream)
-    loss = _empty((1,), torch.float32, dev, stream)
-    num_tokens = _empty((1,), torch.int32, dev, stream)
+    idx = _empty(logits, (t, top_k), torch.int32, stream)
+    weights = _empty(logits, (t, top_k), torch.float32, stream)
+    counts = _empty(logits, (e,), torch.int32, stream)
+    loss = _empty(logits, (1,), torch.float32, stream)
+    num_tokens = _empty(logits, (1,), torch.int32, stream)
     if torch._C._cuda_getDevice() == dev.index:
         nbytes = dg_moe_route_workspace_size(t, e)
     else:
         with torch.cuda.device(dev):
             nbytes = dg_moe_route_workspace_size(t, e)
-    ws = _empty((nbytes,), torch.uint8, dev, stream) if nbytes else None
+    ws = _empty(logits, (nbytes,), torch.uint8, stream) if nbytes else None
     _on_device("dg_moe_route",
                (_ptr(logits), _DTYPES[logits.dtype], t, e, ld, top_k, int(bool(normalize)),
                 _ptr(token_mask), _ptr(idx), _ptr(weights), _ptr(counts), _ptr(loss),
@@ -912,7 +913,7 @@ def dg_moe_route_backward(logits, idx, weights, counts, num_tokens, dweights=Non
         if dloss.numel() != 1:
             raise ValueError("dloss must have one element")
         _exact(dloss, "dloss", torch.float32, tuple(dloss.shape))
-    dlogits = _empty((t, e), logits.dtype, logits.device, stream)
+    dlogits = _empty(logits, (t, e), logits.dtype, stream)
     _on_device("dg_moe_route_backward",
                (_ptr(logits), _DTYPES[logits.dtype], t, e, ld, k, int(bool(normalize)), _ptr(idx),
                 _ptr(weights), _ptr(counts), _ptr(num_tokens), _ptr(dweights), _ptr(dloss),

@@ -40,15 +40,17 @@ constexpr int kTurnBytes = 1024;  // per epilogue warp: 16 tokens x 32 columns o
 constexpr int kMaxStages = 12;
 constexpr uint32_t kBBytes = kTileN * kStageK / 2;              // 16 KB
 constexpr uint32_t kSfBBytes = kStageWords * kMxBlockBytes;     // one row block
-// TMEM: 256 accumulator columns (two tiles of up to 128 tokens, or one of
-// 256), then scale slots of 32 columns: B's words at 0 and 4, A's word w of
-// row block b at 8 + 8 w + 4 b.
-constexpr uint32_t kTmemCols = 512;
-constexpr uint32_t kSfCol = 256, kSfSlotCols = 32;
+// TMEM: two accumulators of up to 128 columns (one of 256), then scale slots of
+// 32 columns: B's words at 0 and 4, A's word w of row block b at 8 + 8 w + 4 b.
+constexpr uint32_t kSfSlotCols = 32;
 constexpr int kSfSlots = 4;
-// Shared memory of a launch stays above half an SM's, so that no two CTAs
-// that each want all TMEM columns sit on one SM (a CTA of a cluster waiting
-// for TMEM there while its peers wait for it could deadlock two launches).
+// A CTA takes a whole SM (512 columns) or, with tiles of up to 64 tokens, half
+// of one (256 columns, half the registers and shared memory).  The shared
+// memory of a whole one stays above half an SM's, so that no two CTAs that
+// together want more than the 512 columns sit on one SM: a CTA of a cluster
+// that waits for TMEM there while its peers wait for it could deadlock two
+// launches.
+constexpr int kHalfTokens = 64;
 constexpr int kMinSmem = 120 * 1024;
 
 // A dense launch of several waves may leave its last tiles to a second launch.
@@ -199,8 +201,8 @@ __device__ __forceinline__ int mma_n(const Tile &t) {
 // PAIR: two CTAs of a cluster compute a tile of 256 rows of B with
 // cta_group::2 MMAs issued by rank 0; each loads its 128 rows of B and half of
 // the tokens, so an SM moves 32 KB per stage instead of 48 KB.
-template <int SCHED, bool PAIR>
-__global__ void __launch_bounds__(kThreads, 1)
+template <int SCHED, bool PAIR, bool HALF>
+__global__ void __launch_bounds__(kThreads, HALF ? 2 : 1)
 mxfp4_gemm_kernel(const __grid_constant__ CUtensorMap tmap_a,
                   const __grid_constant__ CUtensorMap tmap_b,
                   const __grid_constant__ CUtensorMap tmap_sfa,
@@ -218,9 +220,9 @@ mxfp4_gemm_kernel(const __grid_constant__ CUtensorMap tmap_a,
   const uint32_t stage_bytes = kBBytes + a_bytes;
   const uint32_t sf_stage = kSfBBytes + (p.tok_tile > 128 ? 2 * kSfBBytes : kSfBBytes);
   const uint32_t sf_base = base + static_cast<uint32_t>(p.stages) * stage_bytes;
-  int *s_table = reinterpret_cast<int *>(
-      smem_raw + (sf_base - raw) + static_cast<uint32_t>(p.stages) * sf_stage);
-  __shared__ __align__(16) uint8_t s_turn[kEpiWarps * kTurnBytes];
+  // the epilogue's turning area, then the tables
+  const uint32_t turn_base = sf_base + static_cast<uint32_t>(p.stages) * sf_stage;
+  int *s_table = reinterpret_cast<int *>(smem_raw + (turn_base - raw) + kEpiWarps * kTurnBytes);
   const uint32_t bars = smem_u32(s_bars);
   auto full_bar = [&](int s) { return bars + 8u * s; };
   auto empty_bar = [&](int s) { return bars + 8u * (kMaxStages + s); };
@@ -231,7 +233,9 @@ mxfp4_gemm_kernel(const __grid_constant__ CUtensorMap tmap_a,
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const uint32_t rank = PAIR ? cluster_ctarank() : 0;
   const int nbuf = p.tok_tile > 128 ? 1 : 2;
-  const uint32_t buf_cols = p.tok_tile > 128 ? 256u : 128u;
+  const uint32_t buf_cols = HALF ? 64u : p.tok_tile > 128 ? 256u : 128u;
+  constexpr uint32_t tmem_cols = HALF ? 256u : 512u, sf_col = tmem_cols / 2;
+  constexpr int kChunks = (HALF ? kHalfTokens : kMaxTokens) / 32;  // 32 tokens each
   const int a_blocks = (p.rows + 127) / 128, b_blocks = (p.n + 127) / 128;  // per slab / expert
   const int blocks = p.rows / 128;  // contiguous
   Tables tab;
@@ -271,10 +275,10 @@ mxfp4_gemm_kernel(const __grid_constant__ CUtensorMap tmap_a,
   }
   if (warp == 1) {
     if constexpr (PAIR) {
-      tmem_alloc_pair(smem_u32(&s_tmem), kTmemCols);
+      tmem_alloc_pair(smem_u32(&s_tmem), tmem_cols);
       tmem_relinquish_pair();
     } else {
-      tmem_alloc(smem_u32(&s_tmem), kTmemCols);
+      tmem_alloc(smem_u32(&s_tmem), tmem_cols);
       tmem_relinquish();
     }
   }
@@ -440,7 +444,7 @@ mxfp4_gemm_kernel(const __grid_constant__ CUtensorMap tmap_a,
             const uint64_t bdesc = bdesc0 + static_cast<uint32_t>(s) * (stage_bytes >> 4);
             const uint64_t adesc = bdesc + (kBBytes >> 4);
             const uint64_t sfdesc = sfdesc0 + static_cast<uint32_t>(s) * (sf_stage >> 4);
-            const uint32_t slot = tmem + kSfCol + (it % kSfSlots) * kSfSlotCols;
+            const uint32_t slot = tmem + sf_col + (it % kSfSlots) * kSfSlotCols;
             const uint32_t first = ks == t.k_begin ? 1u : 0u;
             auto cp = [&](uint32_t to, uint32_t from) {
               if constexpr (PAIR) tmem_cp_32x128b_x4_pair(slot + to, sfdesc + (from >> 4));
@@ -502,15 +506,15 @@ mxfp4_gemm_kernel(const __grid_constant__ CUtensorMap tmap_a,
     // tokens has the only accumulator, so the MMAs of the next one wait).
     const int half = (warp - kFirstEpiWarp) >> 2;
     const int quarter = warp & 3;
-    const uint32_t turn = smem_u32(s_turn) + (warp - kFirstEpiWarp) * kTurnBytes;
+    const uint32_t turn = turn_base + (warp - kFirstEpiWarp) * kTurnBytes;
     int tile_i = 0;
     for_each_tile<SCHED, PAIR>(p, tab, [&](const Tile &t) {
       const int buf = nbuf == 2 ? tile_i & 1 : 0;
       const uint32_t use = nbuf == 2 ? tile_i >> 1 : tile_i;
       // rows that are stored: bit l of live[i] is token 32 i + l
-      uint32_t live[8];
+      uint32_t live[kChunks];
 #pragma unroll
-      for (int i = 0; i < 8; ++i) {
+      for (int i = 0; i < kChunks; ++i) {
         bool v = 32 * i + lane < t.tokens;
         if (SCHED == kMxContiguous && v)
           v = __ldg(p.m_indices + t.tok0 + 32 * i + lane) == t.group;
@@ -541,9 +545,9 @@ mxfp4_gemm_kernel(const __grid_constant__ CUtensorMap tmap_a,
       }
       // out[i]: 16 tokens of the warp's 32 columns, as 8 x 8 matrices: [4 h + m],
       // h the 16-lane half, m = 2 (token / 8) + (column / 8) within it
-      uint32_t out[8][8];
+      uint32_t out[kChunks][8];
 #pragma unroll
-      for (int i = 0; i < 8; i += 2) {
+      for (int i = 0; i < kChunks; i += 2) {
         uint32_t r[2][16];
 #pragma unroll
         for (int q = 0; q < 2; ++q) {
@@ -584,7 +588,7 @@ mxfp4_gemm_kernel(const __grid_constant__ CUtensorMap tmap_a,
       const int n = t.n0 + quarter * 32 + 8 * (lane & 3);
       uint16_t *dst = p.d + (static_cast<int64_t>(t.slab) * p.rows + t.tok0 + tok) * p.n + n;
 #pragma unroll
-      for (int i = 0; i < 8; ++i) {
+      for (int i = 0; i < kChunks; ++i) {
         const int c0 = (2 * i + half) * 16;
         if (c0 < t.tokens) {
           stmatrix_x4_trans(st_a, out[i][0], out[i][1], out[i][2], out[i][3]);
@@ -646,8 +650,8 @@ mxfp4_gemm_kernel(const __grid_constant__ CUtensorMap tmap_a,
   if constexpr (PAIR) cluster_sync();
   tc_fence_after();
   if (warp == 1) {
-    if constexpr (PAIR) tmem_dealloc_pair(tmem, kTmemCols);
-    else tmem_dealloc(tmem, kTmemCols);
+    if constexpr (PAIR) tmem_dealloc_pair(tmem, tmem_cols);
+    else tmem_dealloc(tmem, tmem_cols);
   }
   if (p.tail == kIsTail) grid_dependency_wait();
 }
@@ -696,11 +700,11 @@ constexpr int kMaxDevices = 64;
 // shared memory, eight bytes a block); more rows are several launches.
 constexpr int kMaxContiguousRows = 2048 * 128;
 
-template <int SCHED, bool PAIR>
+template <int SCHED, bool PAIR, bool HALF>
 int configure(int dev, int smem) {
   static bool done[kMaxDevices] = {};
   if (done[dev]) return DG_OK;
-  if (cudaFuncSetAttribute(mxfp4_gemm_kernel<SCHED, PAIR>,
+  if (cudaFuncSetAttribute(mxfp4_gemm_kernel<SCHED, PAIR, HALF>,
                            cudaFuncAttributeMaxDynamicSharedMemorySize, smem) != cudaSuccess)
     return DG_ERR_CUDA;
   done[dev] = true;
@@ -709,7 +713,7 @@ int configure(int dev, int smem) {
 
 // Most clusters of `size` CTAs (2 .. 8) with all shared memory that are resident
 // at once; asked once per device, kernel and size.
-template <int SCHED, bool PAIR>
+template <int SCHED, bool PAIR, bool HALF>
 int clusters_fit(int dev, int size, int smem) {
   static int fit[kMaxDevices][9] = {};  // count + 1; 0 = not asked yet
   if (fit[dev][size] == 0) {
@@ -725,7 +729,7 @@ int clusters_fit(int dev, int size, int smem) {
     q.attrs = a;
     q.numAttrs = 1;
     int n = 0;
-    if (cudaOccupancyMaxActiveClusters(&n, mxfp4_gemm_kernel<SCHED, PAIR>, &q) != cudaSuccess) {
+    if (cudaOccupancyMaxActiveClusters(&n, mxfp4_gemm_kernel<SCHED, PAIR, HALF>, &q) != cudaSuccess) {
       cudaGetLastError();
       n = 0;
     }
@@ -734,14 +738,23 @@ int clusters_fit(int dev, int size, int smem) {
   return fit[dev][size] - 1;
 }
 
-// CTAs of a cluster that split K, at most `most`, for `tiles` tiles of one wave.
-template <int SCHED>
-int pick_splits(int dev, int tiles, int k_stages, int sms, int most, int smem) {
+// CTAs of a cluster that split K, for `tiles` tiles of one wave.
+template <int SCHED, bool HALF>
+int pick_splits(int dev, int tiles, int k_stages, int sms, int smem) {
   int s = sms / tiles;
-  if (s > most) s = most;
+  if (s > 8) s = 8;
   if (s > k_stages) s = k_stages;
-  while (s > 1 && clusters_fit<SCHED, false>(dev, s, smem) < tiles) --s;
+  while (s > 1 && clusters_fit<SCHED, false, HALF>(dev, s, smem) < tiles) --s;
   return s;
+}
+
+// Whether tiles of `tok_tile` tokens run two CTAs per SM: where there are more
+// than SMs, so that the tiles past one per SM start at once and each CTA's
+// latencies overlap the other's (64 x 24576 x 4096, 192 tiles: 13.1 against
+// 19.9 us; but 148 tiles, 64 x 18944 x 16384: 33.9 against 28.8 us, for half
+// the stages each).  A cap on the SMs keeps one.
+bool half_sms(int tok_tile, int64_t tiles, int sms, int all_sms) {
+  return tok_tile <= kHalfTokens && tiles > sms && sms == all_sms;
 }
 
 struct Operands {
@@ -750,18 +763,24 @@ struct Operands {
 };
 
 // Fills in the shapes that follow from p and launches `grid` CTAs.
-template <int SCHED, bool PAIR>
-int launch_form(const Operands &o, MxParams p, int grid, int max_smem, cudaStream_t stream) {
+// Dynamic shared memory that a CTA may take: all of an SM's, or half.
+struct Smem {
+  int full, half;
+};
+
+template <int SCHED, bool PAIR, bool HALF>
+int launch_form(const Operands &o, MxParams p, int grid, const Smem &max, cudaStream_t stream) {
   const int a_rows = PAIR ? p.tok_tile / 2 : p.tok_tile;
   const int stage = static_cast<int>(kBBytes) + a_rows * (kStageK / 2) +
                     static_cast<int>(kSfBBytes) * (p.tok_tile > 128 ? 3 : 2);
-  const int tables = SCHED == kMxMasked       ? (p.groups + 1) * 4
-                     : SCHED == kMxContiguous ? p.rows / 128 * 8
-                                              : 0;
-  p.stages = (max_smem - 1024 - tables) / stage;
+  const int besides = 1024 + kEpiWarps * kTurnBytes +
+                      (SCHED == kMxMasked       ? (p.groups + 1) * 4
+                       : SCHED == kMxContiguous ? p.rows / 128 * 8
+                                                : 0);
+  p.stages = ((HALF ? max.half : max.full) - besides) / stage;
   if (p.stages > kMaxStages) p.stages = kMaxStages;
-  int smem = 1024 + p.stages * stage + tables;
-  if (smem < kMinSmem) smem = kMinSmem;
+  int smem = besides + p.stages * stage;
+  if (!HALF && smem < kMinSmem) smem = kMinSmem;
   CUtensorMap ta, tb, tsa, tsb;
   const int slabs = SCHED == kMxMasked ? p.groups : 1;
   int rc = make_tmap(&ta, o.a, p.k, p.rows, slabs, a_rows);
@@ -784,7 +803,7 @@ int launch_form(const Operands &o, MxParams p, int grid, int max_smem, cudaStrea
   attr[1].val.clusterDim.z = 1;
   cfg.attrs = attr;
   cfg.numAttrs = cluster > 1 ? 2 : 1;
-  return cudaLaunchKernelEx(&cfg, mxfp4_gemm_kernel<SCHED, PAIR>, ta, tb, tsa, tsb, p) ==
+  return cudaLaunchKernelEx(&cfg, mxfp4_gemm_kernel<SCHED, PAIR, HALF>, ta, tb, tsa, tsb, p) ==
                  cudaSuccess
              ? DG_OK
              : DG_ERR_CUDA;
@@ -797,10 +816,17 @@ int launch_mxfp4(const Operands &o, MxParams p, cudaStream_t stream) {
   if (!info || cudaGetDevice(&dev) != cudaSuccess || dev < 0 || dev >= kMaxDevices)
     return DG_ERR_CUDA;
   const int sms = effective_num_sms();
-  // (the barriers and the epilogue's turning area are static)
-  const int max_smem = info->max_smem_optin - kEpiWarps * kTurnBytes - 512;
-  int rc = configure<SCHED, false>(dev, max_smem);
-  if (!rc && SCHED != kMxMasked) rc = configure<SCHED, SCHED != kMxMasked>(dev, max_smem);
+  static int per_sm[kMaxDevices] = {};
+  if (per_sm[dev] == 0 && cudaDeviceGetAttribute(&per_sm[dev],
+                                                 cudaDevAttrMaxSharedMemoryPerMultiprocessor,
+                                                 dev) != cudaSuccess)
+    return DG_ERR_CUDA;
+  // less the barriers (static), and the kilobyte that the system takes per CTA
+  const Smem max = {info->max_smem_optin - 512, per_sm[dev] / 2 - 1024 - 512};
+  int rc = configure<SCHED, false, false>(dev, max.full);
+  if (!rc && SCHED != kMxContiguous)
+    rc = configure<SCHED, false, SCHED != kMxContiguous>(dev, max.half);
+  if (!rc && SCHED != kMxMasked) rc = configure<SCHED, SCHED != kMxMasked, false>(dev, max.full);
   if (rc) return rc;
   const int k_stages = ceil_div(p.k, kStageK);
   // tokens per tile: the smallest power of two that holds all of them
@@ -808,41 +834,44 @@ int launch_mxfp4(const Operands &o, MxParams p, cudaStream_t stream) {
   while (p.tok_tile < kMaxTokens && p.tok_tile < p.rows) p.tok_tile *= 2;
   p.splits = 1;
   p.width = 1;
+  p.n_tiles = ceil_div(p.n, kTileN);
   if constexpr (SCHED == kMxMasked) {
-    p.n_tiles = ceil_div(p.n, kTileN);
-    return launch_form<SCHED, false>(o, p, sms, max_smem, stream);
+    return half_sms(p.tok_tile, static_cast<int64_t>(p.groups) * p.n_tiles, sms, info->num_sms)
+               ? launch_form<SCHED, false, true>(o, p, 2 * sms, max, stream)
+               : launch_form<SCHED, false, false>(o, p, sms, max, stream);
   } else {
     // pairs that are resident at once
-    int pairs = clusters_fit<SCHED, true>(dev, 2, max_smem);
+    int pairs = clusters_fit<SCHED, true, false>(dev, 2, max.full);
     if (pairs > sms / 2) pairs = sms / 2;
     if constexpr (SCHED == kMxContiguous) {
       const int most = p.rows / 128;  // blocks that may hold an expert's rows
-      p.n_tiles = ceil_div(p.n, 2 * kTileN);
-      if (pairs > 0 && ceil_div(most, 2) * p.n_tiles >= 2 * pairs) {
+      const int n_pairs = ceil_div(p.n, 2 * kTileN);
+      if (pairs > 0 && ceil_div(most, 2) * n_pairs >= 2 * pairs) {
         p.tok_tile = 256;
         p.width = 2;
-        return launch_form<SCHED, true>(o, p, 2 * pairs, max_smem, stream);
+        p.n_tiles = n_pairs;
+        return launch_form<SCHED, true, false>(o, p, 2 * pairs, max, stream);
       }
       // few tiles: 128 tokens each, for more of them
       p.tok_tile = 128;
-      p.n_tiles = ceil_div(p.n, kTileN);
       const int tiles = most * p.n_tiles;
-      return launch_form<SCHED, false>(o, p, tiles < sms ? tiles : sms, max_smem, stream);
+      return launch_form<SCHED, false, false>(o, p, tiles < sms ? tiles : sms, max, stream);
     } else {
       p.tok_tiles = ceil_div(p.rows, p.tok_tile);
-      p.n_tiles = ceil_div(p.n, 2 * kTileN);
       p.units = p.tok_tiles * p.n_tiles;
-      const bool pair = p.tok_tile == 256 && pairs > 0 && p.units >= pairs;
+      if (half_sms(p.tok_tile, p.units, sms, info->num_sms))
+        return launch_form<SCHED, false, true>(o, p, p.units < 2 * sms ? p.units : 2 * sms, max,
+                                               stream);
+      const int pair_units = p.tok_tiles * ceil_div(p.n, 2 * kTileN);
+      const bool pair = p.tok_tile == 256 && pairs > 0 && pair_units >= pairs;
       if (pair) {
         p.width = 2;
-      } else {
-        p.n_tiles = ceil_div(p.n, kTileN);
-        p.units = p.tok_tiles * p.n_tiles;
-        // fewer tiles than SMs: split K over the CTAs of a cluster
-        p.splits = p.units < sms
-                       ? pick_splits<SCHED>(dev, p.units, k_stages, sms, 8, max_smem)
-                       : 1;
-        if (p.splits > 1) return launch_form<SCHED, false>(o, p, p.units * p.splits, max_smem, stream);
+        p.n_tiles = ceil_div(p.n, 2 * kTileN);
+        p.units = pair_units;
+      } else if (p.units < sms) {
+        p.splits = pick_splits<SCHED, false>(dev, p.units, k_stages, sms, max.full);
+        if (p.splits > 1)
+          return launch_form<SCHED, false, false>(o, p, p.units * p.splits, max, stream);
       }
       // Whole waves, then the rest split along K in a second launch that fills
       // the SMs as they come free: a last wave of few tiles takes 1/S of a
@@ -853,7 +882,7 @@ int launch_mxfp4(const Operands &o, MxParams p, cudaStream_t stream) {
       const int rest = p.units % wave;
       MxParams t = p;
       if (p.units > wave && rest > 0) {
-        t.splits = pick_splits<SCHED>(dev, rest * p.width, k_stages, sms, 8, max_smem);
+        t.splits = pick_splits<SCHED, false>(dev, rest * p.width, k_stages, sms, max.full);
         if (t.splits > 1 && k_stages - k_stages / t.splits >= kTailCost) {
           t.tail = kIsTail;
           t.unit0 = p.units - rest;
@@ -863,10 +892,10 @@ int launch_mxfp4(const Operands &o, MxParams p, cudaStream_t stream) {
         }
       }
       const int grid = p.units < wave ? p.units : wave;
-      rc = pair ? launch_form<SCHED, true>(o, p, 2 * grid, max_smem, stream)
-                : launch_form<SCHED, false>(o, p, grid, max_smem, stream);
+      rc = pair ? launch_form<SCHED, true, false>(o, p, 2 * grid, max, stream)
+                : launch_form<SCHED, false, false>(o, p, grid, max, stream);
       if (rc || p.tail == kAlone) return rc;
-      return launch_form<SCHED, false>(o, t, rest * t.width * t.splits, max_smem, stream);
+      return launch_form<SCHED, false, false>(o, t, rest * t.width * t.splits, max, stream);
     }
   }
 }
