@@ -547,7 +547,7 @@ int dg_get_device_status(dg_stream_t stream, int *status);
  *   q          device uint8 [batch][M][K/2].
  *   sf         device int32 [batch][ceil(M/128)][ceil(K/128)][32][4], written
  *              whole.
- *   batch >= 1, M >= 0 (0 is a no-op), K > 0, K % 32 == 0, all <= 2^31 - 65536; q and
+ *   batch >= 1, M >= 0 (0 is a no-op), K > 0, K % 32 == 0, all <= 2^31 - 2^20; q and
  *   sf 16-byte aligned.  Deterministic.
  */
 int dg_quantize_mxfp4(const void *x, int x_dtype, int64_t batch, int64_t M,

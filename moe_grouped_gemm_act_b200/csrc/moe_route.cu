@@ -46,9 +46,11 @@ constexpr int kFinishCtas = 8;  // one cluster
 constexpr int kClusterTokens = 4 * kWarps * kFinishCtas;
 
 // Resident blocks per SM that an instance with V experts per lane is compiled
-// for: a token is a chain of shuffles and warp maxima, so warps, not
-// instructions, hide its latency.
-constexpr int resident(int v) { return v <= 4 ? 4 : v == 8 ? 3 : v == 16 ? 2 : 1; }
+// for: a token is a chain of shuffles and warp maxima whose latency other warps
+// hide, but fewer registers than these leave spill (V = 8 with three blocks:
+// 28.4 us against 26.3 us for 32768 tokens of 256 experts; V = 2 with two: 23.4
+// against 18.4 us for 64 experts).
+constexpr int resident(int v) { return v <= 2 ? 4 : v == 4 ? 3 : v == 8 ? 2 : 1; }
 
 // Order-preserving key of an FP32 value that is not NaN; -0 and +0 are one key.
 __device__ __forceinline__ uint32_t order_key(float x) {

@@ -417,9 +417,10 @@ int check_device() {
   return d->ok ? DG_OK : DG_ERR_UNSUPPORTED_ARCH;
 }
 
-// Sizes past which a coordinate would leave 31 bits or an index in elements 62.
+// Sizes past which a coordinate (and a grid's stride past it) would leave 31 bits,
+// or an index in elements 62.
 bool too_large(int64_t batch, int64_t rows, int64_t cols) {
-  constexpr int64_t kMost = 0x7FFF0000;
+  constexpr int64_t kMost = 0x7FF00000;
   return batch > kMost || rows > kMost || cols > kMost ||
          (rows > 0 && cols > 0 && batch > (int64_t(1) << 62) / rows / cols);
 }

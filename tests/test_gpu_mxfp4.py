@@ -52,6 +52,31 @@ def rnd(shape, seed, outliers=False):
     return inputs.activations(int(np.prod(shape[:-1])), shape[-1], seed, outliers).reshape(shape)
 
 
+def blocked(byte):
+    """mxfp4.scale_words on the device, for large operands: [R, K/32] -> words."""
+    r, kg = byte.shape
+    full = torch.zeros((-(-r // 128) * 128, -(-kg // 4) * 4), dtype=torch.uint8, device="cuda")
+    full[:r, :kg] = byte
+    w = full.view(-1, 4, 32, full.shape[1] // 4, 4).permute(0, 3, 2, 1, 4).contiguous()
+    return w.view(torch.int32).squeeze(-1)
+
+
+def random_operand(rows, k, seed):
+    """(q, sf) with random codes and scales, and the values in FP32 (exact)."""
+    gen = torch.Generator(device="cuda").manual_seed(seed)
+    q = torch.randint(0, 256, (rows, k // 2), generator=gen, device="cuda", dtype=torch.uint8)
+    byte = torch.randint(120, 135, (rows, k // 32), generator=gen, device="cuda",
+                         dtype=torch.uint8)
+    v = dev(mxfp4.VALUES).float()[torch.stack([q & 15, q >> 4], -1).flatten(1).int()]
+    v *= torch.exp2(byte.float() - 127).repeat_interleave(32, 1)
+    return q, blocked(byte), v
+
+
+def test_blocked_is_scale_words():
+    byte = np.random.default_rng(0).integers(0, 256, (300, 13)).astype(np.uint8)
+    assert np.array_equal(blocked(dev(byte)).cpu().numpy(), mxfp4.scale_words(byte))
+
+
 # ------------------------------------------------------------------ quantizers
 def special_rows(m, k, seed):
     x = rnd((m, k), seed, outliers=True)
@@ -147,6 +172,82 @@ def test_gemm(m, n, k):
     dg.dg_mxfp4_gemm_nt(qa, sa, qb, sb, again)
     assert torch.equal(again.view(torch.int16), d.contiguous().view(torch.int16))
     assert dg.dg_get_device_status() == 0
+
+
+@pytest.mark.parametrize("m,n,k", [
+    (2500, 2008, 3328),     # whole waves of CTA pairs, then a split tail
+    (100, 24576, 4096),     # the same with single CTAs
+    (17, 20000, 1312),      # two CTAs per SM
+    (700, 7168, 7168), (4096, 4096, 1056)])
+def test_gemm_large(m, n, k):
+    qa, sa, a = random_operand(m, k, 1)
+    qb, sb, b = random_operand(n, k, 2)
+    big = sentinel(m + 2, n)
+    d = big[1:m + 1]
+    for _ in range(2):
+        d.view(torch.int16).fill_(SENTINEL)
+        dg.dg_mxfp4_gemm_nt(qa, sa, qb, sb, d)
+        rows = torch.unique(torch.cat([torch.arange(0, m, 37), torch.tensor([m - 1])])).cuda()
+        check(d[rows], a[rows].double(), b.double(), f"{m}x{n}x{k}")
+        assert not bool((d.view(torch.int16) == SENTINEL).any())
+    assert untouched(big[0]) and untouched(big[-1])
+    assert dg.dg_get_device_status() == 0
+
+
+def test_tail_launch_is_ordered_with_its_neighbours():
+    """The split tail overlaps the launch before it: what follows on the stream must
+    see both, and both must see what came before."""
+    m, n, k = 2500, 2008, 3328
+    qb, sb, b = random_operand(n, k, 3)
+    a32 = [torch.randn(m, k, device="cuda") for _ in range(3)]
+    d = torch.empty((m, n), dtype=torch.bfloat16, device="cuda")
+    q = torch.empty((m, k // 2), dtype=torch.uint8, device="cuda")
+    sf = torch.empty((20, 26, 32, 4), dtype=torch.int32, device="cuda")
+    want = []
+    for x in a32:
+        dg.dg_quantize_mxfp4(x, q=q, sf=sf)
+        dg.dg_mxfp4_gemm_nt(q, sf, qb, sb, d)
+        torch.cuda.synchronize()
+        want.append(d.clone())
+    for _ in range(5):
+        got = []
+        for x in a32:
+            dg.dg_quantize_mxfp4(x, q=q, sf=sf)
+            dg.dg_mxfp4_gemm_nt(q, sf, qb, sb, d)
+            got.append(d.clone())
+        assert all(torch.equal(u, v) for u, v in zip(got, want))
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        dg.dg_quantize_mxfp4(a32[1], q=q, sf=sf)
+        dg.dg_mxfp4_gemm_nt(q, sf, qb, sb, d)
+        copy = d.clone()
+    for _ in range(3):
+        d.zero_()
+        graph.replay()
+        torch.cuda.synchronize()
+        assert torch.equal(copy, want[1])
+
+
+def test_offsets_past_32_bits():
+    """An input and an output of more than 2^32 bytes (2.3e9 elements each)."""
+    m, n, k = 70000, 32768, 64
+    qa, sa, a = random_operand(m, k, 4)
+    qb, sb, b = random_operand(n, k, 5)
+    d = torch.empty((m, n), dtype=torch.bfloat16, device="cuda")
+    dg.dg_mxfp4_gemm_nt(qa, sa, qb, sb, d)
+    rows = torch.tensor([0, 1, 32767, 65536, 65537, 69887, 69999], device="cuda")
+    check(d[rows], a[rows].double(), b.double())
+    q, sf = dg.dg_quantize_mxfp4(d)       # rows of D as an operand
+    x = d[rows].float().cpu().numpy()
+    codes, byte = mxfp4.quantize(x)
+    assert np.array_equal(q[rows].cpu().numpy(), mxfp4.pack(codes))
+    y = dg.dg_dequantize_mxfp4(q, sf)
+    assert np.array_equal(y[rows].double().cpu().numpy(), mxfp4.values(codes, byte))
+    del y
+    cut = d[:69984, 32700:]               # the operand's rows are d's last columns
+    q, sf = dg.dg_quantize_mxfp4(cut, transpose=True)
+    codes, byte = mxfp4.quantize(cut[-96:].float().cpu().numpy().T.copy())
+    assert np.array_equal(q[:, -48:].cpu().numpy(), mxfp4.pack(codes))
 
 
 @pytest.mark.parametrize("m,n,k", [(3, 264, 7168), (64, 256, 4096), (200, 256, 7168),
@@ -282,7 +383,8 @@ def test_contiguous_bad_indices_are_reported():
 @pytest.mark.parametrize("counts,m_max,n,k", [
     ([1], 1, 8, 32), ([0, 0], 5, 72, 96), ([3, 0, 16, 9], 16, 264, 160),
     ([100, 1, 0, 57, 99], 100, 1000, 544), ([256, 0, 128, 129, 17], 256, 512, 1056),
-    ([300, 257, 0, 1], 300, 136, 288), ([7] * 40, 30, 128, 256)])
+    ([300, 257, 0, 1], 300, 136, 288), ([7] * 40, 30, 128, 256),
+    (list(range(40)), 40, 520, 96), ([64, 0, 33] * 10, 64, 1032, 160)])
 def test_masked(counts, m_max, n, k):
     g = len(counts)
     x = rnd((g, m_max, k), 17)
