@@ -654,20 +654,22 @@ def dg_m_grouped_fp8_gemm_nt_masked_ue8m0(a, sfa, b, sfb, d, masked_m,
 
 # ------------------------------------------------------------------ MXFP4, routing
 _DTYPES = {torch.float32: DG_DTYPE_F32, torch.bfloat16: DG_DTYPE_BF16}
+_U8, _I32, _F32, _BF16 = torch.uint8, torch.int32, torch.float32, torch.bfloat16
 
 
-def _on_device(name, fn_args, *ts, stream=None):
+def _on_device(name, fn_args, ts, stream):
     """Calls entry point `name` with fn_args and the stream, on the device that
-    the tensors ts (None allowed) share: their own current stream if none is
-    given, whatever device is current.  (The raw-stream and current-device
+    the tensors ts share: their own current stream if none is given, whatever
+    device is current.  (The raw-stream and current-device
     lookups are the ones under torch.cuda's, without their argument handling,
     which took a third of a small call.)"""
     dev = ts[0].get_device()  # (-1: on the host)
+    if dev < 0:
+        raise ValueError("all tensors must be CUDA tensors (there is no CPU path)")
     for t in ts:
-        if t is not None and t.get_device() != dev or dev < 0:
-            if dev < 0 or t.get_device() < 0:
-                raise ValueError("all tensors must be CUDA tensors (there is no CPU path)")
-            raise ValueError(f"tensors on cuda:{dev} and {t.device}: all must be on one device")
+        if t.get_device() != dev:
+            raise ValueError(f"tensors on cuda:{dev} and {t.device}: all must be CUDA tensors on "
+                             f"one device")
     if stream is None:
         raw = torch._C._cuda_getCurrentRawStream(dev)
     elif stream.device.index != dev:
@@ -723,7 +725,7 @@ def _rows_2d(x, name):
 
 def _mx_scales(rows, k):
     """The shape of an operand's MXFP4 scale words."""
-    return (-(-rows // 128), -(-k // 128), 32, 4)
+    return ((rows + 127) // 128, (k + 127) // 128, 32, 4)
 
 
 def dg_quantize_mxfp4(x: torch.Tensor, transpose: bool = False, q=None, sf=None, stream=None):
@@ -749,14 +751,16 @@ def dg_quantize_mxfp4(x: torch.Tensor, transpose: bool = False, q=None, sf=None,
     if lead == (0,):
         raise ValueError("an empty batch")
     if q is None:
-        q = _empty(x, lead + (m, k // 2), torch.uint8, stream)
+        q = _empty(x, lead + (m, k // 2), _U8, stream)
+    else:
+        _exact(q, "q", _U8, lead + (m, k // 2))
     if sf is None:
-        sf = _empty(x, lead + _mx_scales(m, k), torch.int32, stream)
-    _exact(q, "q", torch.uint8, lead + (m, k // 2))
-    _exact(sf, "sf", torch.int32, lead + _mx_scales(m, k))
+        sf = _empty(x, lead + _mx_scales(m, k), _I32, stream)
+    else:
+        _exact(sf, "sf", _I32, lead + _mx_scales(m, k))
     _on_device("dg_quantize_mxfp4",
-               (_ptr(x), _DTYPES[x.dtype], lead[0] if lead else 1, m, k, ld, int(transpose),
-                _ptr(q), _ptr(sf)), x, q, sf, stream=stream)
+               (x.data_ptr(), _DTYPES[x.dtype], lead[0] if lead else 1, m, k, ld, int(transpose),
+                q.data_ptr(), sf.data_ptr()), (x, q, sf), stream)
     return q, sf
 
 
@@ -776,23 +780,33 @@ def dg_dequantize_mxfp4(q: torch.Tensor, sf: torch.Tensor, dtype: torch.dtype = 
         raise ValueError(f"K = {k} must be a positive multiple of 32")
     if lead == (0,):
         raise ValueError("an empty batch")
+    _exact(q, "q", _U8, lead + (m, kh))
+    _exact(sf, "sf", _I32, lead + _mx_scales(m, k))
     if out is None:
         out = _empty(q, lead + (m, k), dtype, stream)
-    _exact(q, "q", torch.uint8, lead + (m, kh))
-    _exact(sf, "sf", torch.int32, lead + _mx_scales(m, k))
-    _exact(out, "out", dtype, lead + (m, k))
+    else:
+        _exact(out, "out", dtype, lead + (m, k))
     _on_device("dg_dequantize_mxfp4",
-               (_ptr(q), _ptr(sf), lead[0] if lead else 1, m, k, _ptr(out), _DTYPES[dtype], k),
-               q, sf, out, stream=stream)
+               (q.data_ptr(), sf.data_ptr(), lead[0] if lead else 1, m, k, out.data_ptr(),
+                _DTYPES[dtype], k), (q, sf, out), stream)
     return out
 
 
 def _mx_operands(a, sfa, b, sfb, d, m, n, k, lead_a, lead_b):
-    _exact(a, "a", torch.uint8, lead_a + (m, k // 2))
-    _exact(sfa, "sfa", torch.int32, lead_a + _mx_scales(m, k))
-    _exact(b, "b", torch.uint8, lead_b + (n, k // 2))
-    _exact(sfb, "sfb", torch.int32, lead_b + _mx_scales(n, k))
-    _exact(d, "d", torch.bfloat16, lead_a + (m, n))
+    """Checks the operands, scales and result of a product; the one expression
+    first, since its parts are half of a small call's time one by one."""
+    sa, sb = lead_a + _mx_scales(m, k), lead_b + _mx_scales(n, k)
+    if (a.dtype is _U8 and b.dtype is _U8 and sfa.dtype is _I32 and sfb.dtype is _I32
+            and d.dtype is _BF16 and b.shape == lead_b + (n, k // 2) and sfa.shape == sa
+            and sfb.shape == sb and d.shape == lead_a + (m, n)
+            and a.shape == lead_a + (m, k // 2) and a.is_contiguous() and b.is_contiguous()
+            and sfa.is_contiguous() and sfb.is_contiguous() and d.is_contiguous()):
+        return
+    _exact(a, "a", _U8, lead_a + (m, k // 2))
+    _exact(sfa, "sfa", _I32, sa)
+    _exact(b, "b", _U8, lead_b + (n, k // 2))
+    _exact(sfb, "sfb", _I32, sb)
+    _exact(d, "d", _BF16, lead_a + (m, n))
 
 
 def dg_mxfp4_gemm_nt(a, sfa, b, sfb, d, stream=None) -> torch.Tensor:
@@ -804,8 +818,8 @@ def dg_mxfp4_gemm_nt(a, sfa, b, sfb, d, stream=None) -> torch.Tensor:
     m, k, n = a.shape[0], 2 * a.shape[1], b.shape[0]
     _mx_operands(a, sfa, b, sfb, d, m, n, k, (), ())
     _on_device("dg_mxfp4_gemm_nt",
-               (_ptr(a), _ptr(sfa), _ptr(b), _ptr(sfb), _ptr(d), m, n, k),
-               a, sfa, b, sfb, d, stream=stream)
+               (a.data_ptr(), sfa.data_ptr(), b.data_ptr(), sfb.data_ptr(), d.data_ptr(), m, n, k),
+               (a, sfa, b, sfb, d), stream)
     return d
 
 
@@ -819,10 +833,10 @@ def dg_m_grouped_mxfp4_gemm_nt_contiguous(a, sfa, b, sfb, d, m_indices,
     m, k = a.shape[0], 2 * a.shape[1]
     g, n = b.shape[:2]
     _mx_operands(a, sfa, b, sfb, d, m, n, k, (), (g,))
-    _exact(m_indices, "m_indices", torch.int32, (m,))
+    _exact(m_indices, "m_indices", _I32, (m,))
     _on_device("dg_m_grouped_mxfp4_gemm_nt_contiguous",
-               (_ptr(a), _ptr(sfa), _ptr(b), _ptr(sfb), _ptr(d), _ptr(m_indices), m, n, k, g),
-               a, sfa, b, sfb, d, m_indices, stream=stream)
+               (a.data_ptr(), sfa.data_ptr(), b.data_ptr(), sfb.data_ptr(), d.data_ptr(),
+                m_indices.data_ptr(), m, n, k, g), (a, sfa, b, sfb, d, m_indices), stream)
     return d
 
 
@@ -835,10 +849,10 @@ def dg_m_grouped_mxfp4_gemm_nt_masked(a, sfa, b, sfb, d, masked_m, stream=None) 
     g, m, k = a.shape[0], a.shape[1], 2 * a.shape[2]
     n = b.shape[1]
     _mx_operands(a, sfa, b, sfb, d, m, n, k, (g,), (g,))
-    _exact(masked_m, "masked_m", torch.int32, (g,))
+    _exact(masked_m, "masked_m", _I32, (g,))
     _on_device("dg_m_grouped_mxfp4_gemm_nt_masked",
-               (_ptr(a), _ptr(sfa), _ptr(b), _ptr(sfb), _ptr(d), _ptr(masked_m), g, m, n, k),
-               a, sfa, b, sfb, d, masked_m, stream=stream)
+               (a.data_ptr(), sfa.data_ptr(), b.data_ptr(), sfb.data_ptr(), d.data_ptr(),
+                masked_m.data_ptr(), g, m, n, k), (a, sfa, b, sfb, d, masked_m), stream)
     return d
 
 
@@ -875,8 +889,8 @@ def dg_moe_route(logits: torch.Tensor, top_k: int, normalize: bool = True, token
         raise ValueError("all tensors must be CUDA tensors (there is no CPU path)")
     # one allocation for the five results (five took half of a small call's time)
     n = t * top_k
-    buf = _empty(logits, (2 * n + e + 2,), torch.int32, stream)
-    real = buf.view(torch.float32)
+    buf = _empty(logits, (2 * n + e + 2,), _I32, stream)
+    real = buf.view(_F32)
     idx = buf.as_strided((t, top_k), (top_k, 1), 0)
     weights = real.as_strided((t, top_k), (top_k, 1), n)
     counts = buf.as_strided((e,), (1,), 2 * n)
@@ -887,11 +901,13 @@ def dg_moe_route(logits: torch.Tensor, top_k: int, normalize: bool = True, token
     else:
         with torch.cuda.device(dev):
             nbytes = dg_moe_route_workspace_size(t, e)
-    ws = _empty(logits, (nbytes,), torch.uint8, stream) if nbytes else None
+    ws = _empty(logits, (nbytes,), _U8, stream) if nbytes else None
+    at = buf.data_ptr()
     _on_device("dg_moe_route",
-               (_ptr(logits), _DTYPES[logits.dtype], t, e, ld, top_k, int(bool(normalize)),
-                _ptr(token_mask), _ptr(idx), _ptr(weights), _ptr(counts), _ptr(loss),
-                _ptr(num_tokens), _ptr(ws), nbytes), logits, token_mask, stream=stream)
+               (logits.data_ptr(), _DTYPES[logits.dtype], t, e, ld, top_k, 1 if normalize else 0,
+                _ptr(token_mask), at, at + 4 * n, at + 8 * n, at + 4 * (2 * n + e + 1),
+                at + 4 * (2 * n + e), _ptr(ws), nbytes),
+               (logits,) if token_mask is None else (logits, token_mask), stream)
     return idx, weights, counts, loss, num_tokens
 
 
@@ -904,20 +920,22 @@ def dg_moe_route_backward(logits, idx, weights, counts, num_tokens, dweights=Non
     if idx.dim() != 2:
         raise ValueError(f"idx must be [T, top_k], got shape {tuple(idx.shape)}")
     k = idx.shape[1]
-    _exact(idx, "idx", torch.int32, (t, k))
-    _exact(weights, "weights", torch.float32, (t, k))
-    _exact(counts, "counts", torch.int32, (e,))
-    _exact(num_tokens, "num_tokens", torch.int32, (1,))
+    ts = [logits, idx, weights, counts, num_tokens]
+    _exact(idx, "idx", _I32, (t, k))
+    _exact(weights, "weights", _F32, (t, k))
+    _exact(counts, "counts", _I32, (e,))
+    _exact(num_tokens, "num_tokens", _I32, (1,))
     if dweights is not None:
-        _exact(dweights, "dweights", torch.float32, (t, k))
+        _exact(dweights, "dweights", _F32, (t, k))
+        ts.append(dweights)
     if dloss is not None:
         if dloss.numel() != 1:
             raise ValueError("dloss must have one element")
-        _exact(dloss, "dloss", torch.float32, tuple(dloss.shape))
+        _exact(dloss, "dloss", _F32, dloss.shape)
+        ts.append(dloss)
     dlogits = _empty(logits, (t, e), logits.dtype, stream)
     _on_device("dg_moe_route_backward",
-               (_ptr(logits), _DTYPES[logits.dtype], t, e, ld, k, int(bool(normalize)), _ptr(idx),
-                _ptr(weights), _ptr(counts), _ptr(num_tokens), _ptr(dweights), _ptr(dloss),
-                _ptr(dlogits)), logits, idx, weights, counts, num_tokens, dweights, dloss,
-               stream=stream)
+               (logits.data_ptr(), _DTYPES[logits.dtype], t, e, ld, k, 1 if normalize else 0,
+                idx.data_ptr(), weights.data_ptr(), counts.data_ptr(), num_tokens.data_ptr(),
+                _ptr(dweights), _ptr(dloss), dlogits.data_ptr()), ts, stream)
     return dlogits
