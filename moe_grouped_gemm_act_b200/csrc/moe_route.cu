@@ -21,7 +21,8 @@
 // keys; the lowest lane that holds the maximum has the lowest index.  Sums over
 // tokens are exact (counts) or taken in a fixed order (probabilities: per lane
 // over a warp's tokens, over the warps of a block, over the blocks), so a
-// repeated call gives the same bits.
+// repeated call gives the same bits.  Loads are coherent (no __ldg): the kernels start
+// before the ones ahead of them on the stream have finished.
 #include <cuda_bf16.h>
 #include <cuda_runtime.h>
 
@@ -86,11 +87,11 @@ __device__ __forceinline__ void load_row(const float *row, int E, bool vec, floa
 #pragma unroll
       for (int i = 0; i < V; i += S) {
         if constexpr (S == 4) {
-          const float4 t = e0 < E ? __ldg(reinterpret_cast<const float4 *>(row + e0 + i))
+          const float4 t = e0 < E ? __ldcg(reinterpret_cast<const float4 *>(row + e0 + i))
                                   : make_float4(-INFINITY, -INFINITY, -INFINITY, -INFINITY);
           x[i] = t.x; x[i + 1] = t.y; x[i + 2] = t.z; x[i + 3] = t.w;
         } else {
-          const float2 t = e0 < E ? __ldg(reinterpret_cast<const float2 *>(row + e0 + i))
+          const float2 t = e0 < E ? __ldcg(reinterpret_cast<const float2 *>(row + e0 + i))
                                   : make_float2(-INFINITY, -INFINITY);
           x[i] = t.x; x[i + 1] = t.y;
         }
@@ -99,7 +100,7 @@ __device__ __forceinline__ void load_row(const float *row, int E, bool vec, floa
     }
   }
 #pragma unroll
-  for (int i = 0; i < V; ++i) x[i] = e0 + i < E ? __ldg(row + e0 + i) : -INFINITY;
+  for (int i = 0; i < V; ++i) x[i] = e0 + i < E ? row[e0 + i] : -INFINITY;
 }
 __device__ __forceinline__ void unpack_bf16(uint32_t w, float &a, float &b) {
   a = __uint_as_float(w << 16);
@@ -115,19 +116,19 @@ __device__ __forceinline__ void load_row(const __nv_bfloat16 *row, int E, bool v
 #pragma unroll
       for (int i = 0; i < V; i += S) {
         if constexpr (S == 8) {
-          const uint4 t = e0 < E ? __ldg(reinterpret_cast<const uint4 *>(row + e0 + i))
+          const uint4 t = e0 < E ? __ldcg(reinterpret_cast<const uint4 *>(row + e0 + i))
                                  : make_uint4(kNegInf2, kNegInf2, kNegInf2, kNegInf2);
           unpack_bf16(t.x, x[i], x[i + 1]);
           unpack_bf16(t.y, x[i + 2], x[i + 3]);
           unpack_bf16(t.z, x[i + 4], x[i + 5]);
           unpack_bf16(t.w, x[i + 6], x[i + 7]);
         } else if constexpr (S == 4) {
-          const uint2 t = e0 < E ? __ldg(reinterpret_cast<const uint2 *>(row + e0 + i))
+          const uint2 t = e0 < E ? __ldcg(reinterpret_cast<const uint2 *>(row + e0 + i))
                                  : make_uint2(kNegInf2, kNegInf2);
           unpack_bf16(t.x, x[i], x[i + 1]);
           unpack_bf16(t.y, x[i + 2], x[i + 3]);
         } else {
-          const uint32_t t = e0 < E ? __ldg(reinterpret_cast<const uint32_t *>(row + e0 + i))
+          const uint32_t t = e0 < E ? __ldcg(reinterpret_cast<const uint32_t *>(row + e0 + i))
                                     : kNegInf2;
           unpack_bf16(t, x[i], x[i + 1]);
         }
@@ -138,9 +139,9 @@ __device__ __forceinline__ void load_row(const __nv_bfloat16 *row, int E, bool v
 #pragma unroll
   for (int i = 0; i < V; ++i)
     x[i] = e0 + i < E
-               ? __uint_as_float(static_cast<uint32_t>(__ldg(
-                                     reinterpret_cast<const unsigned short *>(row) + e0 + i))
-                                 << 16)
+               ? __uint_as_float(
+                     static_cast<uint32_t>(reinterpret_cast<const unsigned short *>(row)[e0 + i])
+                     << 16)
                : -INFINITY;
 }
 

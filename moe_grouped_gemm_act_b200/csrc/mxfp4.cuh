@@ -6,6 +6,11 @@
 // 1, 1.5, 2, 3, 4, 6 and their negatives; two per byte, the element of the
 // lower K index in the low nibble) with one UE8M0 scale 2^(e - 127) per 32
 // consecutive K elements; scale byte 255 is NaN.
+//
+// These kernels start before the ones ahead of them on the stream have finished
+// (programmatic dependent launch), so they read global memory with coherent
+// loads (__ldcg, __ldcs) only: __ldg may use lines that were cached before the
+// data was written.
 #pragma once
 
 #include <cuda_runtime.h>

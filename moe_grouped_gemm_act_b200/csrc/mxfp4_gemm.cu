@@ -131,7 +131,7 @@ __device__ __forceinline__ void for_each_tile(const MxParams &p, const Tables &t
       const int r = u - tab.prefix[lo];
       const int tt = (tab.prefix[lo + 1] - tab.prefix[lo]) / p.n_tiles;  // token tiles
       const int nt = r / tt;
-      const int m = min(__ldg(p.masked_m + lo), p.rows);
+      const int m = min(__ldcg(p.masked_m + lo), p.rows);
       t.slab = t.group = lo;
       t.n0 = nt * kTileN;
       t.tok0 = (r - nt * tt) * p.tok_tile;
@@ -295,7 +295,7 @@ mxfp4_gemm_kernel(const __grid_constant__ CUtensorMap tmap_a,
         const int e = e0 + lane;
         int v = 0;
         if (e < p.groups) {
-          const int m = __ldg(p.masked_m + e);
+          const int m = __ldcg(p.masked_m + e);
           if (m < 0 || m > p.rows) record_status(p.status, DG_ERR_DEVICE_DATA);
           v = (min(max(m, 0), p.rows) + p.tok_tile - 1) / p.tok_tile * p.n_tiles;
         }
@@ -320,7 +320,7 @@ mxfp4_gemm_kernel(const __grid_constant__ CUtensorMap tmap_a,
 #pragma unroll
       for (int j = 0; j < kAtOnce; ++j) {
         const int b = b0 + j * kWarps;
-        if (b < blocks) v[j] = __ldg(idx + static_cast<int64_t>(b) * 32 + lane);
+        if (b < blocks) v[j] = __ldcg(idx + static_cast<int64_t>(b) * 32 + lane);
       }
 #pragma unroll
       for (int j = 0; j < kAtOnce; ++j) {
@@ -517,7 +517,7 @@ mxfp4_gemm_kernel(const __grid_constant__ CUtensorMap tmap_a,
       for (int i = 0; i < kChunks; ++i) {
         bool v = 32 * i + lane < t.tokens;
         if (SCHED == kMxContiguous && v)
-          v = __ldg(p.m_indices + t.tok0 + 32 * i + lane) == t.group;
+          v = __ldcg(p.m_indices + t.tok0 + 32 * i + lane) == t.group;
         live[i] = __ballot_sync(0xffffffffu, v);
       }
       if (!mbar_wait(tfull_bar(buf), use & 1, abort, p.status)) return false;

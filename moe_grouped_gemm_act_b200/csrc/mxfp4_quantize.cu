@@ -373,7 +373,7 @@ dequantize_mxfp4_kernel(const uint8_t *__restrict__ q, const uint32_t *__restric
         word[i] = 0;
         if (k < K) {
           code[i] = __ldcs(reinterpret_cast<const uint2 *>(qrow + i * (kReadPass / 2)));
-          word[i] = __ldg(srow + static_cast<int64_t>(k / 128) * kMxBlockWords);
+          word[i] = __ldcg(srow + static_cast<int64_t>(k / 128) * kMxBlockWords);
         }
       }
 #pragma unroll
