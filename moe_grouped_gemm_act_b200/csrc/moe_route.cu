@@ -76,7 +76,8 @@ __device__ __forceinline__ float warp_sum(float v) {
   return v;
 }
 
-// Experts l V .. l V + V - 1 of a row of E logits, -inf past E.  `vec`: rows
+// Experts l V .. l V + V - 1 of a row of E logits, -inf past E.  (Through L1: a lane's
+// pieces share sectors.)  `vec`: rows
 // start on a 16-byte boundary (or V elements, if that is less) and E % V == 0.
 template <int V>
 __device__ __forceinline__ void load_row(const float *row, int E, bool vec, float x[V]) {
@@ -87,11 +88,11 @@ __device__ __forceinline__ void load_row(const float *row, int E, bool vec, floa
 #pragma unroll
       for (int i = 0; i < V; i += S) {
         if constexpr (S == 4) {
-          const float4 t = e0 < E ? __ldcg(reinterpret_cast<const float4 *>(row + e0 + i))
+          const float4 t = e0 < E ? *reinterpret_cast<const float4 *>(row + e0 + i)
                                   : make_float4(-INFINITY, -INFINITY, -INFINITY, -INFINITY);
           x[i] = t.x; x[i + 1] = t.y; x[i + 2] = t.z; x[i + 3] = t.w;
         } else {
-          const float2 t = e0 < E ? __ldcg(reinterpret_cast<const float2 *>(row + e0 + i))
+          const float2 t = e0 < E ? *reinterpret_cast<const float2 *>(row + e0 + i)
                                   : make_float2(-INFINITY, -INFINITY);
           x[i] = t.x; x[i + 1] = t.y;
         }
@@ -116,19 +117,19 @@ __device__ __forceinline__ void load_row(const __nv_bfloat16 *row, int E, bool v
 #pragma unroll
       for (int i = 0; i < V; i += S) {
         if constexpr (S == 8) {
-          const uint4 t = e0 < E ? __ldcg(reinterpret_cast<const uint4 *>(row + e0 + i))
+          const uint4 t = e0 < E ? *reinterpret_cast<const uint4 *>(row + e0 + i)
                                  : make_uint4(kNegInf2, kNegInf2, kNegInf2, kNegInf2);
           unpack_bf16(t.x, x[i], x[i + 1]);
           unpack_bf16(t.y, x[i + 2], x[i + 3]);
           unpack_bf16(t.z, x[i + 4], x[i + 5]);
           unpack_bf16(t.w, x[i + 6], x[i + 7]);
         } else if constexpr (S == 4) {
-          const uint2 t = e0 < E ? __ldcg(reinterpret_cast<const uint2 *>(row + e0 + i))
+          const uint2 t = e0 < E ? *reinterpret_cast<const uint2 *>(row + e0 + i)
                                  : make_uint2(kNegInf2, kNegInf2);
           unpack_bf16(t.x, x[i], x[i + 1]);
           unpack_bf16(t.y, x[i + 2], x[i + 3]);
         } else {
-          const uint32_t t = e0 < E ? __ldcg(reinterpret_cast<const uint32_t *>(row + e0 + i))
+          const uint32_t t = e0 < E ? *reinterpret_cast<const uint32_t *>(row + e0 + i)
                                     : kNegInf2;
           unpack_bf16(t, x[i], x[i + 1]);
         }
@@ -161,6 +162,11 @@ struct RouteParams {
   int *status;
 };
 
+// A warp's row of shared memory: lane l's V words start at l row_step(V), whose
+// multiples of 16 bytes are odd so that 16-byte accesses do not meet in a bank.
+__host__ __device__ constexpr int row_step(int v) { return v >= 8 ? v + 4 : v; }
+__host__ __device__ constexpr int row_words(int v) { return 32 * row_step(v); }
+
 __device__ __forceinline__ float loss_of(const RouteParams &p, float total, int n) {
   const float nf = static_cast<float>(n);
   return n > 0 ? total * (static_cast<float>(p.experts) /
@@ -172,10 +178,76 @@ __device__ __forceinline__ float loss_of(const RouteParams &p, float total, int 
 // (The kernel is bound by the ALU pipe -- compares, selects and integer maxima
 // -- so a round has few of them per expert.)
 //
-// FP32 logits: the maximum of the lanes' largest keys, then the lowest expert
-// among those that hold it.
-template <typename T, int V>
+// kRow: a lane keeps its largest key, the others wait in the warp's
+// row of shared memory.  A round is a warp maximum; the lowest lane that holds
+// it owns the lowest such expert, and the warp looks up the owner's V keys
+// together, takes the chosen one out and finds the owner's next: some twenty
+// instructions whatever V.
+enum Form { kRow, kRegisters, kWords };
+template <typename T, int V, int FORM>
 struct TopK {
+  uint32_t top;
+  uint32_t *row;  // [row_words(V)]
+  // Experts past E hold -inf, like closed ones.
+  __device__ __forceinline__ void init(const float x[V], uint32_t *warp_row) {
+    row = warp_row;
+    uint32_t key[V];
+    top = 0;
+#pragma unroll
+    for (int i = 0; i < V; ++i) {
+      key[i] = order_key(x[i]);
+      top = max(top, key[i]);
+    }
+    uint32_t *mine = row + (threadIdx.x & 31) * row_step(V);
+    if constexpr (V >= 4) {
+#pragma unroll
+      for (int i = 0; i < V; i += 4)
+        *reinterpret_cast<uint4 *>(mine + i) =
+            make_uint4(key[i], key[i + 1], key[i + 2], key[i + 3]);
+    } else {
+#pragma unroll
+      for (int i = 0; i < V; ++i) mine[i] = key[i];
+    }
+  }
+  // The row's largest logit (-inf: no expert is open).
+  __device__ __forceinline__ float largest() const {
+    return key_value(__reduce_max_sync(0xffffffffu, top));
+  }
+  // The K largest, choice j to lane j: its expert (-1: none) and logit.
+  __device__ __forceinline__ void choose(int K, int &expert, float &value) {
+    const int lane = threadIdx.x & 31;
+    uint32_t mine = kKeyNegInf;
+    expert = -1;
+    __syncwarp();  // the row is written
+    for (int j = 0; j < K; ++j) {
+      const uint32_t best = __reduce_max_sync(0xffffffffu, top);
+      if (best <= kKeyNegInf) break;  // only closed experts are left
+      const int owner = __ffs(__ballot_sync(0xffffffffu, top == best)) - 1;
+      uint32_t *owned = row + owner * row_step(V);
+      uint32_t key = lane < V ? owned[lane] : 0u;
+      const int at = __ffs(__ballot_sync(0xffffffffu, key == best)) - 1;
+      if (lane == j) {
+        expert = owner * V + at;
+        mine = best;
+      }
+      if (lane == at) {
+        key = 0;
+        owned[at] = 0;
+      }
+      const uint32_t next = __reduce_max_sync(0xffffffffu, key);
+      if (lane == owner) top = next;
+      __syncwarp();
+    }
+    value = key_value(mine);
+  }
+};
+// Few experts per lane: the keys stay in registers, and every lane takes the
+// choice out and finds its largest again (32 experts, FP32: 3.7 us a call of 64
+// tokens against 4.3 us; from V = 4 on the form above is faster: 128 experts, 8
+// choices 27.3 against 28.1 us for 32768 tokens, 1024 experts, 16 choices 35
+// against 65 us for 8192).
+template <typename T, int V>
+struct TopK<T, V, kRegisters> {
   uint32_t key[V], top;
   int at;  // the lane's lowest expert with key == top
   __device__ __forceinline__ void find_top() {
@@ -188,24 +260,21 @@ struct TopK {
       if (key[i] == top) at = i;
     at += (threadIdx.x & 31) * V;
   }
-  // Experts past E hold -inf, like closed ones.
-  __device__ __forceinline__ void init(const float x[V]) {
+  __device__ __forceinline__ void init(const float x[V], uint32_t *) {
 #pragma unroll
     for (int i = 0; i < V; ++i) key[i] = order_key(x[i]);
     find_top();
   }
-  // The row's largest logit (-inf: no expert is open).
   __device__ __forceinline__ float largest() const {
     return key_value(__reduce_max_sync(0xffffffffu, top));
   }
-  // The K largest, choice j to lane j: its expert (-1: none) and logit.
   __device__ __forceinline__ void choose(int K, int &expert, float &value) {
     const int lane = threadIdx.x & 31;
     uint32_t mine = kKeyNegInf;
     expert = -1;
     for (int j = 0; j < K; ++j) {
       const uint32_t best = __reduce_max_sync(0xffffffffu, top);
-      if (best <= kKeyNegInf) break;  // only closed experts are left
+      if (best <= kKeyNegInf) break;
       const int e = static_cast<int>(__reduce_min_sync(
           0xffffffffu, top == best ? static_cast<uint32_t>(at) : 0xFFFFFFFFu));
       if (lane == j) {
@@ -226,7 +295,7 @@ struct TopK {
 // others negative, that is larger as unsigned numbers, so the unsigned maximum
 // is the next choice and taking it out is one subtraction per word.
 template <int V>
-struct TopK<__nv_bfloat16, V> {
+struct TopK<__nv_bfloat16, V, kWords> {
   uint32_t rel[V], top, base;
   __device__ __forceinline__ void find_top() {
     top = rel[0];
@@ -234,7 +303,7 @@ struct TopK<__nv_bfloat16, V> {
     for (int i = 1; i + 1 < V; i += 2) top = max(max(top, rel[i]), rel[i + 1]);
     if constexpr (V % 2 == 0) top = max(top, rel[V - 1]);
   }
-  __device__ __forceinline__ void init(const float x[V]) {
+  __device__ __forceinline__ void init(const float x[V], uint32_t *) {
     const uint32_t low = 1023u - (threadIdx.x & 31) * V;
 #pragma unroll
     for (int i = 0; i < V; ++i) {
@@ -276,13 +345,16 @@ struct TopK<__nv_bfloat16, V> {
 template <typename T, int V, bool CLUSTER>
 __global__ void __launch_bounds__(kThreads, resident(V))
 moe_route_kernel(const RouteParams p) {
-  extern __shared__ float s_mem[];  // [kWarps][E] probability sums, [E] counts
+  // [kWarps][row_words(V)], a warp's keys and then its probability sums; [E] counts
+  extern __shared__ __align__(16) float s_mem[];
+  constexpr int kStride = row_words(V);
+  constexpr int kForm = sizeof(T) == 2 ? kWords : V <= 2 ? kRegisters : kRow;
   __shared__ float s_red[kWarps];
   __shared__ int32_t s_tokens;
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const int E = p.experts, K = p.top_k;
   float *s_psum = s_mem;
-  int32_t *s_counts = reinterpret_cast<int32_t *>(s_mem + kWarps * E);
+  int32_t *s_counts = reinterpret_cast<int32_t *>(s_mem + kWarps * kStride);
   grid_launch_dependents();
   for (int e = threadIdx.x; e < E; e += kThreads) s_counts[e] = 0;
   if (threadIdx.x == 0) s_tokens = 0;
@@ -299,8 +371,8 @@ moe_route_kernel(const RouteParams p) {
        t += stride) {
     float x[V];
     load_row<V>(static_cast<const T *>(p.logits) + t * p.ld, E, p.vec != 0, x);
-    TopK<T, V> topk;
-    topk.init(x);
+    TopK<T, V, kForm> topk;
+    topk.init(x, reinterpret_cast<uint32_t *>(s_psum + warp * kStride));
     const float xmax = topk.largest();
     // a NaN or +inf anywhere makes the sum NaN, and so does a row that is
     // closed altogether
@@ -340,14 +412,14 @@ moe_route_kernel(const RouteParams p) {
   }
 #pragma unroll
   for (int i = 0; i < V; ++i)
-    if (lane * V + i < E) s_psum[warp * E + lane * V + i] = psum[i];
+    s_psum[warp * kStride + lane * V + i] = psum[i];
   if (lane == 0) atomicAdd(&s_tokens, routed);
   __syncthreads();
   // the block's sums, in the first row (a thread reads only its own columns)
   for (int e = threadIdx.x; e < E; e += kThreads) {
     float s = 0.0f;
-#pragma unroll
-    for (int w = 0; w < kWarps; ++w) s += s_psum[w * E + e];
+#pragma unroll 4
+    for (int w = 0; w < kWarps; ++w) s += s_psum[w * kStride + e];
     if constexpr (CLUSTER) {
       s_psum[e] = s;
     } else {
@@ -547,27 +619,60 @@ __device__ __forceinline__ void store_row(__nv_bfloat16 *row, int E, bool vec, c
     if (e0 + i < E) row[e0 + i] = __float2bfloat16_rn(g[i]);
 }
 
+// Lane l's V words of a row of shared memory.
+template <int V>
+__device__ __forceinline__ void row_store(float *row, const float g[V]) {
+  float *mine = row + (threadIdx.x & 31) * row_step(V);
+  if constexpr (V >= 4) {
+#pragma unroll
+    for (int i = 0; i < V; i += 4)
+      *reinterpret_cast<float4 *>(mine + i) = make_float4(g[i], g[i + 1], g[i + 2], g[i + 3]);
+  } else {
+#pragma unroll
+    for (int i = 0; i < V; ++i) mine[i] = g[i];
+  }
+}
+
+// Blocks per SM of the backward kernel.  From V = 16 on the experts' c are in
+// shared memory, so that a lane only keeps its V gradients (BF16, 512 experts:
+// 11.8 against 16.5 us for 16384 tokens); below, in registers (72 experts: 3.7
+// against 4.3 us for 5001).
+constexpr int resident_backward(int v) { return v == 16 ? 2 : resident(v); }
+
 template <typename T, int V>
-__global__ void __launch_bounds__(kThreads, resident(V))
+__global__ void __launch_bounds__(kThreads, resident_backward(V))
 moe_route_backward_kernel(const RouteBackwardParams p) {
-  // a warp's gradient row, for the chosen experts' lanes to add to
+  // a row per warp for its gradients, to which the lanes of the chosen experts
+  // add, then (V >= 16) the experts' c
   extern __shared__ __align__(16) float s_rows[];
+  constexpr bool kShared = V >= 16;
   grid_launch_dependents();
   grid_dependency_wait();
   const int lane = threadIdx.x & 31;
   const int E = p.experts, K = p.top_k;
-  float *row = s_rows + (threadIdx.x >> 5) * (32 * V);
-  float c[V];
+  float *row = s_rows + (threadIdx.x >> 5) * row_words(V);
+  float *s_c = s_rows + kWarps * row_words(V);
+  float c_own[kShared ? 1 : V];
   {
     const int n = *p.num_tokens;
     const float nf = static_cast<float>(n);
     const float f = p.dloss && n > 0
                         ? *p.dloss * (static_cast<float>(E) / (static_cast<float>(K) * nf * nf))
                         : 0.0f;
+    if constexpr (kShared) {
+      for (int e = threadIdx.x; e < 32 * V; e += kThreads)
+        s_c[e / V * row_step(V) + e % V] = e < E ? f * static_cast<float>(p.counts[e]) : 0.0f;
+      __syncthreads();
+    } else {
 #pragma unroll
-    for (int i = 0; i < V; ++i)
-      c[i] = lane * V + i < E ? f * static_cast<float>(p.counts[lane * V + i]) : 0.0f;
+      for (int i = 0; i < V; ++i)
+        c_own[i] = lane * V + i < E ? f * static_cast<float>(p.counts[lane * V + i]) : 0.0f;
+    }
   }
+  auto c = [&](int i) -> float {
+    if constexpr (kShared) return s_c[lane * row_step(V) + i];
+    else return c_own[i];
+  };
   const int64_t stride = static_cast<int64_t>(gridDim.x) * kWarps;
   for (int64_t t = static_cast<int64_t>(blockIdx.x) * kWarps + (threadIdx.x >> 5); t < p.tokens;
        t += stride) {
@@ -589,7 +694,7 @@ moe_route_backward_kernel(const RouteBackwardParams p) {
       for (int i = 0; i < V; ++i) {
         g[i] = expf(g[i] - xmax);
         sum += g[i];
-        pc += g[i] * c[i];
+        pc += g[i] * c(i);
       }
       const float inv = 1.0f / warp_sum(sum);
       const float wdw = warp_sum(w * dw);
@@ -597,22 +702,15 @@ moe_route_backward_kernel(const RouteBackwardParams p) {
       const float minus = warp_sum(pc) * inv + (p.normalize ? 0.0f : wdw);
       const float dv = p.normalize ? w * (dw - wdw) : w * dw;
 #pragma unroll
-      for (int i = 0; i < V; ++i) g[i] = g[i] * inv * (c[i] - minus);
+      for (int i = 0; i < V; ++i) g[i] = g[i] * inv * (c(i) - minus);
       // the chosen experts are distinct, so their lanes' additions do not meet
-      store_row<V>(row, 32 * V, true, g);
+      row_store<V>(row, g);
       __syncwarp();
-      if (my_idx >= 0 && my_idx < E) row[my_idx] += dv;
+      if (my_idx >= 0 && my_idx < E) row[my_idx / V * row_step(V) + my_idx % V] += dv;
       __syncwarp();
-      if constexpr (V >= 4) {
+      const float *mine = row + lane * row_step(V);
 #pragma unroll
-        for (int i = 0; i < V; i += 4) {
-          const float4 u = *reinterpret_cast<const float4 *>(row + lane * V + i);
-          g[i] = u.x; g[i + 1] = u.y; g[i + 2] = u.z; g[i + 3] = u.w;
-        }
-      } else {
-#pragma unroll
-        for (int i = 0; i < V; ++i) g[i] = row[lane * V + i];
-      }
+      for (int i = 0; i < V; ++i) g[i] = mine[i];
       __syncwarp();  // the row is free for the next token
     }
     store_row<V>(static_cast<T *>(p.dlogits) + t * E, E, p.vec != 0, g);
@@ -633,14 +731,15 @@ int per_lane(int experts) {
 }
 
 // Blocks of a launch over `tokens`: all resident, a token per warp at least.
-int token_blocks(int64_t tokens, int experts, int num_sms) {
+int token_blocks(int64_t tokens, int num_sms, int per_sm) {
   const int64_t want = (tokens + kWarps - 1) / kWarps;
-  const int64_t most = static_cast<int64_t>(num_sms) * resident(per_lane(experts));
+  const int64_t most = static_cast<int64_t>(num_sms) * per_sm;
   return static_cast<int>(want < most ? want : most);
 }
 
 int route_blocks(int64_t tokens, int experts, int num_sms) {
-  return tokens <= kClusterTokens ? kFinishCtas : token_blocks(tokens, experts, num_sms);
+  return tokens <= kClusterTokens ? kFinishCtas
+                                  : token_blocks(tokens, num_sms, resident(per_lane(experts)));
 }
 
 // Whether a row's V-element pieces can be loaded whole: they start on a
@@ -677,7 +776,7 @@ int launch(void (*kern)(P), int blocks, int smem, const P &p, cudaStream_t strea
 
 template <typename T, int V>
 int route_instance(const RouteParams &p, int blocks, bool cluster, cudaStream_t stream) {
-  const int smem = (kWarps + 1) * p.experts * 4;
+  const int smem = (kWarps * row_words(V) + p.experts) * 4;
   return cluster ? launch(moe_route_kernel<T, V, true>, blocks, smem, p, stream, blocks)
                  : launch(moe_route_kernel<T, V, false>, blocks, smem, p, stream);
 }
@@ -696,7 +795,7 @@ int route_typed(const RouteParams &p, int blocks, bool cluster, cudaStream_t str
 
 template <typename T, int V>
 int backward_instance(const RouteBackwardParams &p, int blocks, cudaStream_t stream) {
-  return launch(moe_route_backward_kernel<T, V>, blocks, kWarps * 32 * V * 4, p, stream);
+  return launch(moe_route_backward_kernel<T, V>, blocks, (1 + kWarps) * row_words(V) * 4, p, stream);
 }
 
 template <typename T>
@@ -825,7 +924,8 @@ extern "C" int dg_moe_route_backward(const void *logits, int dtype, int64_t T, i
   p.dweights = dweights;
   p.dloss = dloss;
   p.dlogits = dlogits;
-  const int blocks = token_blocks(T, E, effective_num_sms());
+  const int blocks =
+      token_blocks(T, effective_num_sms(), resident_backward(per_lane(E)));
   cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
   return dtype == DG_DTYPE_F32 ? backward_typed<float>(p, blocks, s)
                                : backward_typed<__nv_bfloat16>(p, blocks, s);
