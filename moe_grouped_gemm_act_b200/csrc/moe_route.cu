@@ -564,8 +564,10 @@ struct RouteBackwardParams {
   void *dlogits;          // [tokens][experts]
 };
 
+// A lane's V consecutive gradients.  BF16 gradients of BF16 logits: the one
+// rounding, to nearest even.
 template <int V>
-__device__ __forceinline__ void store_row(float *row, int E, bool vec, const float g[V]) {
+__device__ __forceinline__ void store_piece(float *row, int E, bool vec, const float g[V]) {
   const int e0 = (threadIdx.x & 31) * V;
   if constexpr (V >= 2) {
     if (vec) {
@@ -587,9 +589,8 @@ __device__ __forceinline__ void store_row(float *row, int E, bool vec, const flo
   for (int i = 0; i < V; ++i)
     if (e0 + i < E) row[e0 + i] = g[i];
 }
-// BF16 gradients of BF16 logits: the one rounding, to nearest even.
 template <int V>
-__device__ __forceinline__ void store_row(__nv_bfloat16 *row, int E, bool vec, const float g[V]) {
+__device__ __forceinline__ void store_piece(__nv_bfloat16 *row, int E, bool vec, const float g[V]) {
   const int e0 = (threadIdx.x & 31) * V;
   if constexpr (V >= 2) {
     if (vec) {
@@ -619,6 +620,34 @@ __device__ __forceinline__ void store_row(__nv_bfloat16 *row, int E, bool vec, c
     if (e0 + i < E) row[e0 + i] = __float2bfloat16_rn(g[i]);
 }
 
+__device__ __forceinline__ void store_one(float *p, float v) { *p = v; }
+__device__ __forceinline__ void store_one(__nv_bfloat16 *p, float v) {
+  *p = __float2bfloat16_rn(v);
+}
+__device__ __forceinline__ void store_four(float *p, const float4 &v) {
+  *reinterpret_cast<float4 *>(p) = v;
+}
+__device__ __forceinline__ void store_four(__nv_bfloat16 *p, const float4 &v) {
+  const __nv_bfloat162 lo = __floats2bfloat162_rn(v.x, v.y);
+  const __nv_bfloat162 hi = __floats2bfloat162_rn(v.z, v.w);
+  *reinterpret_cast<uint2 *>(p) = make_uint2(*reinterpret_cast<const uint32_t *>(&lo),
+                                             *reinterpret_cast<const uint32_t *>(&hi));
+}
+// A row of shared memory to E consecutive elements, neighbouring lanes to
+// neighbouring addresses; `row` nullptr: zeros.
+template <int V, typename T>
+__device__ __forceinline__ void store_row(T *out, const float *row, int E, bool vec) {
+  const int lane = threadIdx.x & 31;
+  if (V >= 4 && vec) {
+    for (int e = 4 * lane; e < E; e += 128)
+      store_four(out + e, row ? *reinterpret_cast<const float4 *>(row + e / V * row_step(V) + e % V)
+                              : make_float4(0.0f, 0.0f, 0.0f, 0.0f));
+  } else {
+    for (int e = lane; e < E; e += 32)
+      store_one(out + e, row ? row[e / V * row_step(V) + e % V] : 0.0f);
+  }
+}
+
 // Lane l's V words of a row of shared memory.
 template <int V>
 __device__ __forceinline__ void row_store(float *row, const float g[V]) {
@@ -646,6 +675,11 @@ moe_route_backward_kernel(const RouteBackwardParams p) {
   // add, then (V >= 16) the experts' c
   extern __shared__ __align__(16) float s_rows[];
   constexpr bool kShared = V >= 16;
+  // Gradients leave from the row, neighbouring lanes to neighbouring addresses,
+  // where a lane's own piece is 64 bytes or more (FP32, 1024 experts: 18.4
+  // against 25.4 us for 8192 tokens); smaller pieces leave from the registers
+  // (BF16, 256 experts: 13.0 against 15.4 us for 32768).
+  constexpr bool kFromRow = V * sizeof(T) >= 64;
   grid_launch_dependents();
   grid_dependency_wait();
   const int lane = threadIdx.x & 31;
@@ -677,11 +711,18 @@ moe_route_backward_kernel(const RouteBackwardParams p) {
   for (int64_t t = static_cast<int64_t>(blockIdx.x) * kWarps + (threadIdx.x >> 5); t < p.tokens;
        t += stride) {
     const int my_idx = lane < K ? p.idx[t * K + lane] : -1;
-    float g[V];
+    T *out = static_cast<T *>(p.dlogits) + t * E;
     if (__shfl_sync(0xffffffffu, my_idx, 0) < 0) {
+      if constexpr (kFromRow) {
+        store_row<V>(out, nullptr, E, p.vec != 0);
+      } else {
+        float zero[V];
 #pragma unroll
-      for (int i = 0; i < V; ++i) g[i] = 0.0f;
+        for (int i = 0; i < V; ++i) zero[i] = 0.0f;
+        store_piece<V>(out, E, p.vec != 0, zero);
+      }
     } else {
+      float g[V];
       const float w = my_idx >= 0 ? p.weights[t * K + lane] : 0.0f;
       const float dw = my_idx >= 0 && p.dweights ? p.dweights[t * K + lane] : 0.0f;
       load_row<V>(static_cast<const T *>(p.logits) + t * p.ld, E, p.vec != 0, g);
@@ -708,12 +749,16 @@ moe_route_backward_kernel(const RouteBackwardParams p) {
       __syncwarp();
       if (my_idx >= 0 && my_idx < E) row[my_idx / V * row_step(V) + my_idx % V] += dv;
       __syncwarp();
-      const float *mine = row + lane * row_step(V);
+      if constexpr (kFromRow) {
+        store_row<V>(out, row, E, p.vec != 0);
+      } else {
+        const float *mine = row + lane * row_step(V);
 #pragma unroll
-      for (int i = 0; i < V; ++i) g[i] = mine[i];
+        for (int i = 0; i < V; ++i) g[i] = mine[i];
+        store_piece<V>(out, E, p.vec != 0, g);
+      }
       __syncwarp();  // the row is free for the next token
     }
-    store_row<V>(static_cast<T *>(p.dlogits) + t * E, E, p.vec != 0, g);
   }
 }
 
