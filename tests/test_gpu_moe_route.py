@@ -72,7 +72,8 @@ def check_backward(got, x, p, oi, ow, oc, on, dw, dl, normalize, bf16):
 @pytest.mark.parametrize("t,e,k", [(1, 1, 1), (1, 8, 2), (3, 5, 5), (64, 32, 8), (65, 33, 4),
                                    (127, 72, 6), (300, 128, 8), (200, 160, 6), (130, 256, 8),
                                    (70, 257, 32), (90, 512, 16), (40, 1000, 8), (20, 1024, 32),
-                                   (3000, 16, 2)])
+                                   (3000, 16, 2),
+                                   (256, 64, 4), (257, 64, 4)])
 @pytest.mark.parametrize("normalize", [True, False])
 def test_route_and_gradient(t, e, k, dtype, normalize):
     g = np.random.default_rng(t * e)
