@@ -53,9 +53,6 @@ constexpr int kSfSlots = 4;
 constexpr int kHalfTokens = 64;
 constexpr int kMinSmem = 120 * 1024;
 
-// A dense launch of several waves may leave its last tiles to a second launch.
-enum Tail : int { kAlone = 0, kHasTail = 1, kIsTail = 2 };
-
 struct MxParams {
   uint16_t *d;
   const int32_t *m_indices, *masked_m;
@@ -65,12 +62,9 @@ struct MxParams {
   int groups;
   int tok_tile;      // tokens per tile: 16, 32, 64, 128 or 256
   int tok_tiles;     // dense: ceil(rows / tok_tile)
-  int n_tiles;       // ceil(n / (128 * width))
-  int width;         // 128-row blocks of B per unit: 2 for the pair form and its tail
-  int unit0, units;  // dense: the units (tiles, or pairs of them) of this launch
+  int n_tiles;       // ceil(n / 128), for the pair form ceil(n / 256)
   int stages;
   int splits;        // CTAs of a cluster that split a tile's K (dense; 1: none)
-  int tail;          // dense: kAlone, kHasTail or kIsTail (see launch_mxfp4)
 };
 
 struct Tile {
@@ -122,7 +116,8 @@ __device__ __forceinline__ void for_each_tile(const MxParams &p, const Tables &t
   const int rank = PAIR ? static_cast<int>(cluster_ctarank()) : 0;
   if constexpr (SCHED == kMxMasked) {
     const int units = tab.prefix[p.groups];
-    for (int u = blockIdx.x; u < units; u += gridDim.x) {
+    constexpr int kCtas = PAIR ? 2 : 1;
+    for (int u = blockIdx.x / kCtas; u < units; u += gridDim.x / kCtas) {
       int lo = 0, hi = p.groups - 1;  // largest e with prefix[e] <= u
       while (lo < hi) {
         const int mid = (lo + hi + 1) >> 1;
@@ -133,26 +128,23 @@ __device__ __forceinline__ void for_each_tile(const MxParams &p, const Tables &t
       const int nt = r / tt;
       const int m = min(__ldcg(p.masked_m + lo), p.rows);
       t.slab = t.group = lo;
-      t.n0 = nt * kTileN;
+      t.n0 = (PAIR ? 2 * nt + rank : nt) * kTileN;
       t.tok0 = (r - nt * tt) * p.tok_tile;
       t.tokens = min(p.tok_tile, m - t.tok0);
       if (!f(t)) return;
     }
   } else {
-    // a cluster's CTAs share a unit (a pair) or a tile (each a part of its K);
-    // `parts` tiles make up a unit of the tail of a pair launch
+    // a cluster's CTAs share a tile: a pair its rows of B, a split its K
     const int cluster = PAIR ? 2 : p.splits;
-    const int parts = PAIR ? 1 : p.width;
     const int tok_tiles = SCHED == kMxContiguous ? tab.count : p.tok_tiles;
-    const int total = (SCHED == kMxContiguous ? tok_tiles * p.n_tiles : p.units) * parts;
+    const int units = tok_tiles * p.n_tiles;
     const int first = blockIdx.x / cluster, stride = gridDim.x / cluster;
     if (SCHED == kMxDense && !PAIR && p.splits > 1) {
       const int s = blockIdx.x - first * p.splits;
       t.k_begin = k_stages * s / p.splits;
       t.k_end = k_stages * (s + 1) / p.splits;
     }
-    for (int v = first; v < total; v += stride) {
-      const int u = p.unit0 + v / parts;
+    for (int u = first; u < units; u += stride) {
       // groups of kRaster token tiles, all rows of B for one after another:
       // a wave's tiles share both operands in L2
       constexpr int kRaster = 16;
@@ -161,8 +153,7 @@ __device__ __forceinline__ void for_each_tile(const MxParams &p, const Tables &t
       const int across = min(kRaster, tok_tiles - grp * kRaster);
       const int nt = in / across;
       const int tt = grp * kRaster + in - nt * across;
-      t.n0 = (nt * p.width + (PAIR ? rank : v % parts)) * kTileN;
-      if (!PAIR && t.n0 >= p.n) continue;
+      t.n0 = (PAIR ? 2 * nt + rank : nt) * kTileN;
       if constexpr (SCHED == kMxContiguous) {
         const int entry = tab.list[tt];
         t.tok0 = (entry >> 1) * 128;
@@ -244,7 +235,7 @@ mxfp4_gemm_kernel(const __grid_constant__ CUtensorMap tmap_a,
   tab.list = s_table + blocks;
   tab.count = 0;
 
-  if (p.tail != kHasTail) grid_launch_dependents();
+  grid_launch_dependents();
   if (SCHED == kMxDense && warp == 3) {
     // B's boxes of the first stages are asked into L2 before the set-up and the
     // dependency wait (a prefetch only fills L2, which the previous kernel's
@@ -282,12 +273,7 @@ mxfp4_gemm_kernel(const __grid_constant__ CUtensorMap tmap_a,
       tmem_relinquish();
     }
   }
-  // A tail does not read what the launch before it writes, so it does not wait
-  // for it here: that launch lets it start only once the kernels before both
-  // have completed.  It waits at its own end instead, so that whatever follows
-  // the tail follows both.
-  if (p.tail != kIsTail) grid_dependency_wait();
-  if (p.tail == kHasTail) grid_launch_dependents();
+  grid_dependency_wait();
   if constexpr (SCHED == kMxMasked) {
     if (warp == 2) {
       int running = 0;
@@ -653,7 +639,6 @@ mxfp4_gemm_kernel(const __grid_constant__ CUtensorMap tmap_a,
     if constexpr (PAIR) tmem_dealloc_pair(tmem, tmem_cols);
     else tmem_dealloc(tmem, tmem_cols);
   }
-  if (p.tail == kIsTail) grid_dependency_wait();
 }
 
 // ------------------------------------------------------------------ host side
@@ -826,29 +811,33 @@ int launch_mxfp4(const Operands &o, MxParams p, cudaStream_t stream) {
   int rc = configure<SCHED, false, false>(dev, max.full);
   if (!rc && SCHED != kMxContiguous)
     rc = configure<SCHED, false, SCHED != kMxContiguous>(dev, max.half);
-  if (!rc && SCHED != kMxMasked) rc = configure<SCHED, SCHED != kMxMasked, false>(dev, max.full);
+  if (!rc) rc = configure<SCHED, true, false>(dev, max.full);
   if (rc) return rc;
   const int k_stages = ceil_div(p.k, kStageK);
   // tokens per tile: the smallest power of two that holds all of them
   p.tok_tile = 16;
   while (p.tok_tile < kMaxTokens && p.tok_tile < p.rows) p.tok_tile *= 2;
   p.splits = 1;
-  p.width = 1;
   p.n_tiles = ceil_div(p.n, kTileN);
+  // pairs that are resident at once
+  int pairs = clusters_fit<SCHED, true, false>(dev, 2, max.full);
+  if (pairs > sms / 2) pairs = sms / 2;
   if constexpr (SCHED == kMxMasked) {
-    return half_sms(p.tok_tile, static_cast<int64_t>(p.groups) * p.n_tiles, sms, info->num_sms)
-               ? launch_form<SCHED, false, true>(o, p, 2 * sms, max, stream)
-               : launch_form<SCHED, false, false>(o, p, sms, max, stream);
+    if (half_sms(p.tok_tile, static_cast<int64_t>(p.groups) * p.n_tiles, sms, info->num_sms))
+      return launch_form<SCHED, false, true>(o, p, 2 * sms, max, stream);
+    // (pairs: 32 experts of 7168 x 2048, 200 tokens each 66 -> 61 us, 8 of 4096 x
+    // 7168, 700 tokens each 77 -> 67 us; no faster with tiles of 128 tokens)
+    if (p.tok_tile == 256 && pairs > 0) {
+      p.n_tiles = ceil_div(p.n, 2 * kTileN);
+      return launch_form<SCHED, true, false>(o, p, 2 * pairs, max, stream);
+    }
+    return launch_form<SCHED, false, false>(o, p, sms, max, stream);
   } else {
-    // pairs that are resident at once
-    int pairs = clusters_fit<SCHED, true, false>(dev, 2, max.full);
-    if (pairs > sms / 2) pairs = sms / 2;
     if constexpr (SCHED == kMxContiguous) {
       const int most = p.rows / 128;  // blocks that may hold an expert's rows
       const int n_pairs = ceil_div(p.n, 2 * kTileN);
       if (pairs > 0 && ceil_div(most, 2) * n_pairs >= 2 * pairs) {
         p.tok_tile = 256;
-        p.width = 2;
         p.n_tiles = n_pairs;
         return launch_form<SCHED, true, false>(o, p, 2 * pairs, max, stream);
       }
@@ -858,44 +847,20 @@ int launch_mxfp4(const Operands &o, MxParams p, cudaStream_t stream) {
       return launch_form<SCHED, false, false>(o, p, tiles < sms ? tiles : sms, max, stream);
     } else {
       p.tok_tiles = ceil_div(p.rows, p.tok_tile);
-      p.units = p.tok_tiles * p.n_tiles;
-      if (half_sms(p.tok_tile, p.units, sms, info->num_sms))
-        return launch_form<SCHED, false, true>(o, p, p.units < 2 * sms ? p.units : 2 * sms, max,
+      const int tiles = p.tok_tiles * p.n_tiles;
+      if (half_sms(p.tok_tile, tiles, sms, info->num_sms))
+        return launch_form<SCHED, false, true>(o, p, tiles < 2 * sms ? tiles : 2 * sms, max,
                                                stream);
-      const int pair_units = p.tok_tiles * ceil_div(p.n, 2 * kTileN);
-      const bool pair = p.tok_tile == 256 && pairs > 0 && pair_units >= pairs;
-      if (pair) {
-        p.width = 2;
+      const int pair_tiles = p.tok_tiles * ceil_div(p.n, 2 * kTileN);
+      if (p.tok_tile == 256 && pairs > 0 && pair_tiles >= pairs) {
         p.n_tiles = ceil_div(p.n, 2 * kTileN);
-        p.units = pair_units;
-      } else if (p.units < sms) {
-        p.splits = pick_splits<SCHED, false>(dev, p.units, k_stages, sms, max.full);
-        if (p.splits > 1)
-          return launch_form<SCHED, false, false>(o, p, p.units * p.splits, max, stream);
+        return launch_form<SCHED, true, false>(o, p, 2 * pairs, max, stream);
       }
-      // Whole waves, then the rest split along K in a second launch that fills
-      // the SMs as they come free: a last wave of few tiles takes 1/S of a
-      // wave instead of a whole one.  A split costs about as much as kTailCost
-      // stages (the cluster's reduction), so short K keeps the whole wave.
-      constexpr int kTailCost = 10;
-      const int wave = pair ? pairs : sms;
-      const int rest = p.units % wave;
-      MxParams t = p;
-      if (p.units > wave && rest > 0) {
-        t.splits = pick_splits<SCHED, false>(dev, rest * p.width, k_stages, sms, max.full);
-        if (t.splits > 1 && k_stages - k_stages / t.splits >= kTailCost) {
-          t.tail = kIsTail;
-          t.unit0 = p.units - rest;
-          t.units = rest;
-          p.tail = kHasTail;
-          p.units -= rest;
-        }
+      if (tiles < sms) {
+        p.splits = pick_splits<SCHED, false>(dev, tiles, k_stages, sms, max.full);
+        return launch_form<SCHED, false, false>(o, p, tiles * p.splits, max, stream);
       }
-      const int grid = p.units < wave ? p.units : wave;
-      rc = pair ? launch_form<SCHED, true, false>(o, p, 2 * grid, max, stream)
-                : launch_form<SCHED, false, false>(o, p, grid, max, stream);
-      if (rc || p.tail == kAlone) return rc;
-      return launch_form<SCHED, false, false>(o, t, rest * t.width * t.splits, max, stream);
+      return launch_form<SCHED, false, false>(o, p, sms, max, stream);
     }
   }
 }
@@ -905,8 +870,8 @@ int check_gemm(const void *A, const void *sfa, const void *B, const void *sfb, c
   if (rows < 0 || N <= 0 || K <= 0 || K % kMxGroup != 0 || N % 8 != 0) return DG_ERR_INVALID_ARG;
   if (rows == 0) return DG_OK;
   if (!A || !sfa || !B || !sfb || !D) return DG_ERR_INVALID_ARG;
-  // tile and block counts are 32-bit
-  constexpr int64_t kMost = 0x7FFFFF00;
+  // tile and block counts, and a grid's step past them, are 31-bit
+  constexpr int64_t kMost = 0x7FFFF000;
   if (rows > kMost || N > kMost || K > kMost) return DG_ERR_INVALID_ARG;
   if (mx_row_blocks(rows) * mx_row_blocks(N) * slabs > kMost ||
       mx_row_blocks(N) * groups > kMost || mx_row_blocks(rows) * slabs > kMost)

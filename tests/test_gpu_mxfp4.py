@@ -175,7 +175,7 @@ def test_gemm(m, n, k):
 
 
 @pytest.mark.parametrize("m,n,k", [
-    (2500, 2008, 3328),     # whole waves of CTA pairs, then a split tail
+    (2500, 2008, 3328),     # CTA pairs, a last wave of few tiles
     (100, 24576, 4096),     # the same with single CTAs
     (17, 20000, 1312),      # two CTAs per SM
     (700, 7168, 7168), (4096, 4096, 1056)])
@@ -194,9 +194,9 @@ def test_gemm_large(m, n, k):
     assert dg.dg_get_device_status() == 0
 
 
-def test_tail_launch_is_ordered_with_its_neighbours():
-    """The split tail overlaps the launch before it: what follows on the stream must
-    see both, and both must see what came before."""
+def test_overlapping_launches_are_ordered():
+    """Every kernel starts before the one ahead of it has finished: each must still
+    see all that came before it on the stream."""
     m, n, k = 2500, 2008, 3328
     qb, sb, b = random_operand(n, k, 3)
     a32 = [torch.randn(m, k, device="cuda") for _ in range(3)]
@@ -383,7 +383,7 @@ def test_contiguous_bad_indices_are_reported():
 @pytest.mark.parametrize("counts,m_max,n,k", [
     ([1], 1, 8, 32), ([0, 0], 5, 72, 96), ([3, 0, 16, 9], 16, 264, 160),
     ([100, 1, 0, 57, 99], 100, 1000, 544), ([256, 0, 128, 129, 17], 256, 512, 1056),
-    ([300, 257, 0, 1], 300, 136, 288), ([7] * 40, 30, 128, 256),
+    ([300, 257, 0, 1], 300, 136, 288), ([700, 0, 129, 513, 256], 700, 392, 544), ([7] * 40, 30, 128, 256),
     (list(range(40)), 40, 520, 96), ([64, 0, 33] * 10, 64, 1032, 160)])
 def test_masked(counts, m_max, n, k):
     g = len(counts)
