@@ -176,6 +176,7 @@ def test_gemm(m, n, k):
 
 @pytest.mark.parametrize("m,n,k", [
     (2500, 2008, 3328),     # CTA pairs, a last wave of few tiles
+    (2350, 2008, 800),      # the same, half a tile past the rows
     (100, 24576, 4096),     # the same with single CTAs
     (17, 20000, 1312),      # two CTAs per SM
     (700, 7168, 7168), (4096, 4096, 1056)])
