@@ -44,14 +44,15 @@ constexpr int kMaxTopK = 32;  // lane j keeps choice j
 constexpr int kFinishCtas = 8;  // one cluster
 // Up to this many tokens (two per warp of it) one cluster does everything in one
 // launch; above it a second kernel joins the blocks' sums (256 experts, BF16: 256
-// tokens 6.4 against 6.9 us, 512 tokens 10.1 against 6.9 us).
+// tokens 6.3 against 6.1 us and one launch and one workspace less on the host, 512
+// tokens 10.1 against 6.3 us).
 constexpr int kClusterTokens = 2 * kWarps * kFinishCtas;
 
 // Resident blocks per SM that an instance with V experts per lane is compiled
 // for: a token is a chain of shuffles and warp maxima whose latency other warps
 // hide, but fewer registers than these leave spill (V = 8 with three blocks:
-// 28.4 us against 26.3 us for 32768 tokens of 256 experts; V = 2 with two: 23.4
-// against 18.4 us for 64 experts).
+// 26.8 us against 24.2 us for 32768 tokens of 256 experts; V = 2 with two: 27.9
+// against 17.7 us for 64 experts).
 constexpr int resident(int v) { return v <= 2 ? 4 : v == 4 ? 3 : v == 8 ? 2 : 1; }
 
 // Order-preserving key of an FP32 value that is not NaN; -0 and +0 are one key.
@@ -179,7 +180,10 @@ __device__ __forceinline__ float loss_of(const RouteParams &p, float total, int 
                : 0.0f;
 }
 
-// The choice of the k largest, one per round; no open expert left ends it.
+// The choice of the k largest, one per round; no open expert left ends it.  The
+// first is the row's largest, which the softmax has found, and the last is not
+// taken out (one round less of k: 32768 tokens of 256 experts, BF16, 24.8 -> 24.2
+// us).
 // (The kernel is bound by the ALU pipe -- compares, selects and integer maxima
 // -- so a round has few of them per expert.)
 //
@@ -191,7 +195,7 @@ __device__ __forceinline__ float loss_of(const RouteParams &p, float total, int 
 enum Form { kRow, kRegisters, kWords };
 template <typename T, int V, int FORM>
 struct TopK {
-  uint32_t top;
+  uint32_t top, best;
   uint32_t *row;  // [row_words(V)]
   // Experts past E hold -inf, like closed ones.
   __device__ __forceinline__ void init(const float x[V], uint32_t *warp_row) {
@@ -215,8 +219,9 @@ struct TopK {
     }
   }
   // The row's largest logit (-inf: no expert is open).
-  __device__ __forceinline__ float largest() const {
-    return key_value(__reduce_max_sync(0xffffffffu, top));
+  __device__ __forceinline__ float largest() {
+    best = __reduce_max_sync(0xffffffffu, top);
+    return key_value(best);
   }
   // The K largest, choice j to lane j: its expert (-1: none) and logit.
   __device__ __forceinline__ void choose(int K, int &expert, float &value) {
@@ -224,8 +229,7 @@ struct TopK {
     uint32_t mine = kKeyNegInf;
     expert = -1;
     __syncwarp();  // the row is written
-    for (int j = 0; j < K; ++j) {
-      const uint32_t best = __reduce_max_sync(0xffffffffu, top);
+    for (int j = 0;;) {
       if (best <= kKeyNegInf) break;  // only closed experts are left
       const int owner = __ffs(__ballot_sync(0xffffffffu, top == best)) - 1;
       uint32_t *owned = row + owner * row_step(V);
@@ -235,25 +239,28 @@ struct TopK {
         expert = owner * V + at;
         mine = best;
       }
+      if (++j == K) break;
       if (lane == at) {
         key = 0;
         owned[at] = 0;
       }
       const uint32_t next = __reduce_max_sync(0xffffffffu, key);
       if (lane == owner) top = next;
+      best = __reduce_max_sync(0xffffffffu, top);
       __syncwarp();
     }
+    __syncwarp();  // the row is free
     value = key_value(mine);
   }
 };
 // Few experts per lane: the keys stay in registers, and every lane takes the
-// choice out and finds its largest again (32 experts, FP32: 3.7 us a call of 64
-// tokens against 4.3 us; from V = 4 on the form above is faster: 128 experts, 8
-// choices 27.3 against 28.1 us for 32768 tokens, 1024 experts, 16 choices 35
-// against 65 us for 8192).
+// choice out and finds its largest again (32 experts, FP32: 3.6 us a call of 64
+// tokens against 4.4 us; from V = 4 on the form above is faster: 128 experts, 8
+// choices 24.6 against 27.1 us for 32768 tokens, 1024 experts, 16 choices 28
+// against 55 us for 8192).
 template <typename T, int V>
 struct TopK<T, V, kRegisters> {
-  uint32_t key[V], top;
+  uint32_t key[V], top, best;
   int at;  // the lane's lowest expert with key == top
   __device__ __forceinline__ void find_top() {
     top = key[0];
@@ -270,15 +277,15 @@ struct TopK<T, V, kRegisters> {
     for (int i = 0; i < V; ++i) key[i] = order_key(x[i]);
     find_top();
   }
-  __device__ __forceinline__ float largest() const {
-    return key_value(__reduce_max_sync(0xffffffffu, top));
+  __device__ __forceinline__ float largest() {
+    best = __reduce_max_sync(0xffffffffu, top);
+    return key_value(best);
   }
   __device__ __forceinline__ void choose(int K, int &expert, float &value) {
     const int lane = threadIdx.x & 31;
     uint32_t mine = kKeyNegInf;
     expert = -1;
-    for (int j = 0; j < K; ++j) {
-      const uint32_t best = __reduce_max_sync(0xffffffffu, top);
+    for (int j = 0;;) {
       if (best <= kKeyNegInf) break;
       const int e = static_cast<int>(__reduce_min_sync(
           0xffffffffu, top == best ? static_cast<uint32_t>(at) : 0xFFFFFFFFu));
@@ -286,10 +293,12 @@ struct TopK<T, V, kRegisters> {
         expert = e;
         mine = best;
       }
+      if (++j == K) break;
 #pragma unroll
       for (int i = 0; i < V; ++i)
         if (lane * V + i == e) key[i] = 0;
       find_top();
+      best = __reduce_max_sync(0xffffffffu, top);
     }
     value = key_value(mine);
   }
@@ -301,7 +310,7 @@ struct TopK<T, V, kRegisters> {
 // is the next choice and taking it out is one subtraction per word.
 template <int V>
 struct TopK<__nv_bfloat16, V, kWords> {
-  uint32_t rel[V], top, base;
+  uint32_t rel[V], top, best;
   __device__ __forceinline__ void find_top() {
     top = rel[0];
 #pragma unroll
@@ -317,27 +326,29 @@ struct TopK<__nv_bfloat16, V, kWords> {
                             0x80000000u;
       rel[i] = ((u ^ flip) >> 6) + (low - i);
     }
-    base = 0;
     find_top();
   }
   static __device__ __forceinline__ float value_of(uint32_t word) {
     const uint32_t k = (word >> 10) << 16;
     return key_value((k & 0x80000000u) ? k : k | 0xFFFFu);
   }
-  __device__ __forceinline__ float largest() const {
-    return value_of(__reduce_max_sync(0xffffffffu, top));
+  __device__ __forceinline__ float largest() {
+    best = __reduce_max_sync(0xffffffffu, top);
+    return value_of(best);
   }
   __device__ __forceinline__ void choose(int K, int &expert, float &value) {
     const int lane = threadIdx.x & 31;
     uint32_t mine = 0x7Fu << 10;  // -inf's key is 0x7F
-    for (int j = 0; j < K; ++j) {
-      const uint32_t best = __reduce_max_sync(0xffffffffu, top);
-      base += best;
+    uint32_t base = best;
+    for (int j = 0;;) {
       if (base < (0x80u << 10)) break;  // only closed experts are left
       if (lane == j) mine = base;
+      if (++j == K) break;
 #pragma unroll
       for (int i = 0; i < V; ++i) rel[i] -= best;
       find_top();
+      best = __reduce_max_sync(0xffffffffu, top);
+      base += best;
     }
     expert = mine < (0x80u << 10) ? -1 : 1023 - static_cast<int>(mine & 1023u);
     value = value_of(mine);
