@@ -96,6 +96,21 @@ def test_route_and_gradient(t, e, k, dtype, normalize):
     assert dg.dg_get_device_status() == 0
 
 
+
+@pytest.mark.parametrize("dtype", [torch.float32, torch.bfloat16])
+@pytest.mark.parametrize("e,k", [(1, 1), (7, 2), (8, 8), (9, 3), (127, 5), (255, 8), (257, 8),
+                                 (511, 4), (512, 32), (1000, 6), (1023, 1), (1024, 32)])
+def test_joined_blocks(e, k, dtype):
+    """Many tokens: the blocks' sums are joined by a second kernel, for every
+    split of the E + 1 columns."""
+    for t in (257, 2500):
+        xd, x = logits(t, e, t + e, dtype, closed=e > 7)
+        mask = np.random.default_rng(e).random(t) < 0.9
+        a, b = (dg.dg_moe_route(xd, k, True, dev(mask)) for _ in range(2))
+        check_forward(a, x, k, True, mask)
+        assert all(torch.equal(u, v) for u, v in zip(a, b))
+    assert dg.dg_get_device_status() == 0
+
 def test_ties_signed_zeros_and_lowest_values():
     low = torch.finfo(torch.float32).min
     x = np.array([[0.0, -0.0, 0.0, -0.0, 1.0, 1.0, 1.0, 1.0],
