@@ -426,6 +426,9 @@ moe_route_kernel(const RouteParams p) {
       p.weights[t * K + lane] = my_w;
     }
   }
+  // A lane's sums lie where other lanes' keys were; after a last token that does not
+  // route nothing else orders these writes behind those of init().
+  __syncwarp();
 #pragma unroll
   for (int i = 0; i < V; ++i)
     s_psum[warp * kStride + lane * V + i] = psum[i];

@@ -111,6 +111,24 @@ def test_joined_blocks(e, k, dtype):
         assert all(torch.equal(u, v) for u, v in zip(a, b))
     assert dg.dg_get_device_status() == 0
 
+
+@pytest.mark.parametrize("dtype", [torch.float32, torch.bfloat16])
+@pytest.mark.parametrize("e", [160, 256, 500, 1024])
+@pytest.mark.parametrize("t", [100, 256, 5000])
+def test_last_token_of_a_warp_does_not_route(t, e, dtype):
+    """The keys of a warp's last token lie where its probability sums go: left out
+    by the mask, by closed experts or by a NaN, it must leave nothing there."""
+    xd, x = logits(t, e, t + e, dtype)
+    first = t // 2                       # every warp's tokens ascend
+    mask = np.arange(t) < first
+    check_forward(dg.dg_moe_route(xd, 8, True, dev(mask)), x, 8, True, mask)
+    assert dg.dg_get_device_status() == 0
+    for hole, status in ((-np.inf, 0), (np.nan, dg.DG_ERR_DEVICE_DATA)):
+        xd[first:], x[first:] = hole, hole
+        check_forward(dg.dg_moe_route(xd, 8), x, 8, True, None)
+        assert dg.dg_get_device_status() == status
+
+
 def test_ties_signed_zeros_and_lowest_values():
     low = torch.finfo(torch.float32).min
     x = np.array([[0.0, -0.0, 0.0, -0.0, 1.0, 1.0, 1.0, 1.0],
