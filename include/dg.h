@@ -658,7 +658,8 @@ int dg_moe_route(const void *logits, int dtype, int64_t T, int E, int64_t ld,
                  int32_t *num_tokens, void *workspace, size_t workspace_bytes,
                  dg_stream_t stream);
 
-/* Scratch bytes of dg_moe_route on the current device. */
+/* Scratch bytes of dg_moe_route on the current device, enough under any SM cap
+ * (dg_set_num_sms); 0 where none is needed and for an E that the call refuses. */
 size_t dg_moe_route_workspace_size(int64_t T, int E);
 
 /*

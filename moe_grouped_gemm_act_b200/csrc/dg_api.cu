@@ -4,6 +4,7 @@
 #include <cuda.h>
 #include <cuda_runtime.h>
 
+#include <atomic>
 #include <cstdint>
 #include <cstdlib>
 #include <mutex>
@@ -21,7 +22,7 @@ namespace {
 constexpr int kMaxDevices = 64;
 DeviceInfo g_info[kMaxDevices];
 std::once_flag g_info_once[kMaxDevices];
-int g_sm_cap = 0;  // dg_set_num_sms; 0 = all
+std::atomic<int> g_sm_cap{0};  // dg_set_num_sms; 0 = all
 
 bool aligned16(const void *p) { return (reinterpret_cast<uintptr_t>(p) & 15u) == 0; }
 

@@ -805,6 +805,11 @@ int route_blocks(int64_t tokens, int experts, int num_sms) {
                                   : token_blocks(tokens, num_sms, resident(per_lane(experts)));
 }
 
+// Scratch of a launch of `blocks`: RouteParams::part.
+size_t part_bytes(int blocks, int experts) {
+  return static_cast<size_t>(blocks) * (static_cast<size_t>(experts) + 1) * sizeof(int2);
+}
+
 // Whether a row's V-element pieces can be loaded whole: they start on a
 // 16-byte boundary (their own size, if less) and none is cut by E.
 int vector_rows(const void *a, const void *b, int64_t ld, int64_t ld_b, int experts, int esz) {
@@ -891,11 +896,11 @@ bool aligned(const void *p, int n) { return reinterpret_cast<uintptr_t>(p) % n =
 
 extern "C" size_t dg_moe_route_workspace_size(int64_t T, int E) {
   using namespace dg;
-  if (T <= kClusterTokens || E < 1) return 0;
-  int sms = effective_num_sms();
-  if (sms <= 0) sms = 148;  // no usable device: size for a full B200
-  const size_t blocks = static_cast<size_t>(route_blocks(T, E, sms));
-  return blocks * (static_cast<size_t>(E) + 1) * sizeof(int2);
+  if (T <= kClusterTokens || E < 1 || E > kMaxExperts) return 0;
+  // for all SMs, whatever the cap: another thread may raise it before the call
+  const DeviceInfo *d = device_info();
+  const int sms = d && d->num_sms > 0 ? d->num_sms : 148;  // (no device: a full B200's)
+  return part_bytes(route_blocks(T, E, sms), E);
 }
 
 extern "C" int dg_moe_route(const void *logits, int dtype, int64_t T, int E, int64_t ld,
@@ -913,9 +918,10 @@ extern "C" int dg_moe_route(const void *logits, int dtype, int64_t T, int E, int
     return DG_ERR_ALIGNMENT;
   rc = check_device();
   if (rc) return rc;
+  // (the cap is read once: the workspace is checked for the blocks that are launched)
   const int blocks = route_blocks(T, E, effective_num_sms());
   const bool cluster = T <= kClusterTokens;
-  if (!cluster && (!workspace || workspace_bytes < dg_moe_route_workspace_size(T, E)))
+  if (!cluster && (!workspace || workspace_bytes < part_bytes(blocks, E)))
     return DG_ERR_WORKSPACE;
   RouteParams p{};
   p.logits = logits;

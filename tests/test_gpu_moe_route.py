@@ -8,6 +8,8 @@ exact.  A gradient is bounded by the same factor times the sum of its terms'
 magnitudes, and BF16 gradients by 2^-8 of the value more.
 """
 
+import threading
+
 import numpy as np
 import pytest
 import torch
@@ -206,6 +208,63 @@ def test_gradient_against_differences():
             continue  # a choice changes here: no derivative
         # FP32 sums of ~t*k terms of size ~1: 2^-20 / 2h, and h^2/6 of the third derivative (< 4)
         assert abs((f(up) - f(dn)) / (2 * h) - float(d[i, j])) < 2.0 ** -11
+
+
+def test_workspace_and_the_sm_cap():
+    """The size holds under every cap, so a cap that changes between the two calls does
+    no harm; results under a cap differ in the loss's rounding alone."""
+    t, e, k = 4000, 96, 4
+    xd, x = logits(t, e, 77)
+    size = dg.dg_moe_route_workspace_size(t, e)
+    try:
+        for cap in (1, 3, 60, 147):
+            dg.dg_set_num_sms(cap)
+            assert dg.dg_moe_route_workspace_size(t, e) == size
+            out = dg.dg_moe_route(xd, k)
+            oi, ow, oc, on, p = check_forward(out, x, k, True, None)
+            dw = np.random.default_rng(1).normal(size=(t, k)).astype(np.float32)
+            d = dg.dg_moe_route_backward(xd, *(out[i] for i in (0, 1, 2, 4)), dev(dw))
+            check_backward(d, x, p, oi, ow, oc, on, dw, None, True, False)
+    finally:
+        dg.dg_set_num_sms(0)
+    assert dg.dg_get_device_status() == 0
+
+
+def test_sm_cap_changed_by_another_thread():
+    """The scratch that is enough for one SM, while another thread moves the cap: a
+    call either has enough or is refused, and nothing behind the scratch is written."""
+    t, e, k = 4000, 64, 4
+    xd, x = logits(t, e, 78)
+    lib = dg.load_library()
+    need = 4 * (e + 1) * 8               # four blocks: what one SM takes
+    ws = torch.full((4 << 20,), 0x5A, dtype=torch.uint8, device="cuda")
+    i32 = lambda n: torch.zeros(n, dtype=torch.int32, device="cuda")
+    idx, w, counts, loss, num = i32(t * k), i32(t * k), i32(e), i32(1), i32(1)
+    assert ws.numel() >= dg.dg_moe_route_workspace_size(t, e)
+    stop = threading.Event()
+
+    def toggle():
+        while not stop.is_set():
+            lib.dg_set_num_sms(1)
+            lib.dg_set_num_sms(0)
+
+    th = threading.Thread(target=toggle)
+    th.start()
+    try:
+        rcs = {lib.dg_moe_route(xd.data_ptr(), 0, t, e, e, k, 1, None, idx.data_ptr(),
+                                w.data_ptr(), counts.data_ptr(), loss.data_ptr(), num.data_ptr(),
+                                ws.data_ptr(), need, None) for _ in range(3000)}
+    finally:
+        stop.set()
+        th.join()
+        dg.dg_set_num_sms(0)
+    torch.cuda.synchronize()
+    assert rcs <= {dg.DG_OK, dg.DG_ERR_WORKSPACE}
+    assert bool((ws[need:] == 0x5A).all())
+    if dg.DG_OK in rcs:
+        out = (idx.view(t, k), w.view(torch.float32).view(t, k), counts,
+               loss.view(torch.float32), num)
+        check_forward(out, x, k, True, None)
 
 
 def test_graph_replay_and_two_graphs():

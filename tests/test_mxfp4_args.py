@@ -2,6 +2,9 @@
 argument checks with addresses that are never dereferenced (every case fails
 before any CUDA call), and the binding's checks of types, shapes and strides."""
 
+import subprocess
+import sys
+
 import pytest
 import torch
 
@@ -146,3 +149,16 @@ def test_binding_refuses_shapes_and_types():
         with pytest.raises(ValueError):
             call()
             pytest.fail(f"call {i} was accepted")
+
+
+def test_route_workspace_size_of_refused_experts():
+    """No scratch for a number of experts that the call refuses -- and an answer (in a
+    child process: a size that never came back would hold up the others)."""
+    code = ("import moe_grouped_gemm_act_b200 as dg\n"
+            "print([dg.dg_moe_route_workspace_size(t, e) for t in (1, 257, 1 << 40)"
+            "       for e in (-1, 0, 1025, (1 << 30) + 1, (1 << 31) - 1)])")
+    r = subprocess.run([sys.executable, "-c", code], capture_output=True, text=True, timeout=300)
+    assert r.returncode == 0, r.stderr
+    assert set(eval(r.stdout)) == {0}
+    for e in (1, 1024):
+        assert dg.dg_moe_route_workspace_size(257, e) > 0
