@@ -819,8 +819,9 @@ int vector_rows(const void *a, const void *b, int64_t ld, int64_t ld_b, int expe
          reinterpret_cast<uintptr_t>(a) % bytes == 0 && reinterpret_cast<uintptr_t>(b) % bytes == 0;
 }
 
+// `most`: the dynamic shared memory of the kernel's largest launch.
 template <typename P>
-int launch(void (*kern)(P), int blocks, int smem, const P &p, cudaStream_t stream,
+int launch(void (*kern)(P), int blocks, int smem, int most, const P &p, cudaStream_t stream,
            int cluster = 1) {
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = dim3(blocks);
@@ -835,18 +836,21 @@ int launch(void (*kern)(P), int blocks, int smem, const P &p, cudaStream_t strea
   attr[1].val.clusterDim.z = 1;
   cfg.attrs = attr;
   cfg.numAttrs = cluster > 1 ? 2 : 1;
-  // (a maximum of more than 48 KB has to be asked for, on each device)
-  if (smem > 48 * 1024 &&
-      cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, smem) != cudaSuccess)
+  // (a maximum of more than 48 KB has to be asked for, on each device; always the
+  // same one, so that threads with launches of different sizes do not lower it for
+  // each other)
+  if (most > 48 * 1024 &&
+      cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, most) != cudaSuccess)
     return DG_ERR_CUDA;
   return cudaLaunchKernelEx(&cfg, kern, p) == cudaSuccess ? DG_OK : DG_ERR_CUDA;
 }
 
 template <typename T, int V>
 int route_instance(const RouteParams &p, int blocks, bool cluster, cudaStream_t stream) {
-  const int smem = (kWarps * row_words(V) + p.experts) * 4;
-  return cluster ? launch(moe_route_kernel<T, V, true>, blocks, smem, p, stream, blocks)
-                 : launch(moe_route_kernel<T, V, false>, blocks, smem, p, stream);
+  const int rows = kWarps * row_words(V) * 4, smem = rows + p.experts * 4;
+  const int most = rows + 32 * V * 4;
+  return cluster ? launch(moe_route_kernel<T, V, true>, blocks, smem, most, p, stream, blocks)
+                 : launch(moe_route_kernel<T, V, false>, blocks, smem, most, p, stream);
 }
 
 template <typename T>
@@ -863,7 +867,8 @@ int route_typed(const RouteParams &p, int blocks, bool cluster, cudaStream_t str
 
 template <typename T, int V>
 int backward_instance(const RouteBackwardParams &p, int blocks, cudaStream_t stream) {
-  return launch(moe_route_backward_kernel<T, V>, blocks, (1 + kWarps) * row_words(V) * 4, p, stream);
+  const int smem = (1 + kWarps) * row_words(V) * 4;
+  return launch(moe_route_backward_kernel<T, V>, blocks, smem, smem, p, stream);
 }
 
 template <typename T>

@@ -230,6 +230,37 @@ def test_workspace_and_the_sm_cap():
     assert dg.dg_get_device_status() == 0
 
 
+@pytest.mark.parametrize("dtype", [torch.float32, torch.bfloat16])
+def test_threads_with_different_experts(dtype):
+    """From 513 experts on, one kernel serves every E with shared memory of its own
+    size: threads that route different E at once must not take each other's."""
+    t, k, lib, rcs = 2, 4, dg.load_library(), {}
+    code = {torch.float32: dg.DG_DTYPE_F32, torch.bfloat16: dg.DG_DTYPE_BF16}[dtype]
+    cases = {e: logits(t, e, e, dtype)[0] for e in (513, 600, 1024)}
+    want = {e: dg.dg_moe_route(x, k) for e, x in cases.items()}
+    bufs = {e: [torch.zeros_like(v) for v in want[e]] for e in cases}
+    streams = {e: torch.cuda.Stream() for e in cases}
+    torch.cuda.synchronize()
+    start = threading.Barrier(len(cases))
+
+    def work(e):
+        i, w, c, ls, n = (v.data_ptr() for v in bufs[e])
+        args = (cases[e].data_ptr(), code, t, e, e, k, 1, None, i, w, c, ls, n, None, 0,
+                streams[e].cuda_stream)
+        start.wait()
+        rcs[e] = {lib.dg_moe_route(*args) for _ in range(50000)}
+
+    threads = [threading.Thread(target=work, args=(e,)) for e in cases]
+    for th in threads:
+        th.start()
+    for th in threads:
+        th.join()
+    torch.cuda.synchronize()
+    assert rcs == {e: {dg.DG_OK} for e in cases}
+    for e in cases:
+        assert all(torch.equal(u, v) for u, v in zip(bufs[e], want[e]))
+
+
 def test_sm_cap_changed_by_another_thread():
     """The scratch that is enough for one SM, while another thread moves the cap: a
     call either has enough or is refused, and nothing behind the scratch is written."""
