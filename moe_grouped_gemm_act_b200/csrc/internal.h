@@ -33,6 +33,14 @@ inline cudaLaunchAttribute pdl_attribute() {
   return a;
 }
 
+// A CUDA call's outcome as a status.  A failure is taken out of the runtime's
+// last-error slot: the next entry point that asks for it would report it as its own.
+inline int cuda_status(cudaError_t e) {
+  if (e == cudaSuccess) return DG_OK;
+  (void)cudaGetLastError();
+  return DG_ERR_CUDA;
+}
+
 // ---------------------------------------------------------------- GEMM
 // kDenseCluster: dense tiles every one split `splits` ways along K, the splits
 // of a tile forming one thread-block cluster that reduces through

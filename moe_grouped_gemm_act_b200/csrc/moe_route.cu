@@ -839,10 +839,12 @@ int launch(void (*kern)(P), int blocks, int smem, int most, const P &p, cudaStre
   // (a maximum of more than 48 KB has to be asked for, on each device; always the
   // same one, so that threads with launches of different sizes do not lower it for
   // each other)
-  if (most > 48 * 1024 &&
-      cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, most) != cudaSuccess)
-    return DG_ERR_CUDA;
-  return cudaLaunchKernelEx(&cfg, kern, p) == cudaSuccess ? DG_OK : DG_ERR_CUDA;
+  if (most > 48 * 1024) {
+    const int rc = cuda_status(
+        cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, most));
+    if (rc) return rc;
+  }
+  return cuda_status(cudaLaunchKernelEx(&cfg, kern, p));
 }
 
 template <typename T, int V>
@@ -960,9 +962,7 @@ extern "C" int dg_moe_route(const void *logits, int dtype, int64_t T, int E, int
   attr[1].val.clusterDim.z = 1;
   cfg.attrs = attr;
   cfg.numAttrs = 2;
-  return cudaLaunchKernelEx(&cfg, moe_route_finish_kernel, p, blocks) == cudaSuccess
-             ? DG_OK
-             : DG_ERR_CUDA;
+  return cuda_status(cudaLaunchKernelEx(&cfg, moe_route_finish_kernel, p, blocks));
 }
 
 extern "C" int dg_moe_route_backward(const void *logits, int dtype, int64_t T, int E, int64_t ld,

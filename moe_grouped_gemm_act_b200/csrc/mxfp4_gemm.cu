@@ -706,11 +706,10 @@ template <int SCHED, bool PAIR, bool HALF>
 int configure(int dev, int smem) {
   static bool done[kMaxDevices] = {};
   if (done[dev]) return DG_OK;
-  if (cudaFuncSetAttribute(mxfp4_gemm_kernel<SCHED, PAIR, HALF>,
-                           cudaFuncAttributeMaxDynamicSharedMemorySize, smem) != cudaSuccess)
-    return DG_ERR_CUDA;
-  done[dev] = true;
-  return DG_OK;
+  const int rc = cuda_status(cudaFuncSetAttribute(
+      mxfp4_gemm_kernel<SCHED, PAIR, HALF>, cudaFuncAttributeMaxDynamicSharedMemorySize, smem));
+  if (!rc) done[dev] = true;
+  return rc;
 }
 
 // Most clusters of `size` CTAs (2 .. 8) with all shared memory that are resident
@@ -805,10 +804,8 @@ int launch_form(const Operands &o, MxParams p, int grid, const Smem &max, cudaSt
   attr[1].val.clusterDim.z = 1;
   cfg.attrs = attr;
   cfg.numAttrs = cluster > 1 ? 2 : 1;
-  return cudaLaunchKernelEx(&cfg, mxfp4_gemm_kernel<SCHED, PAIR, HALF>, ta, tb, tsa, tsb, p) ==
-                 cudaSuccess
-             ? DG_OK
-             : DG_ERR_CUDA;
+  return cuda_status(
+      cudaLaunchKernelEx(&cfg, mxfp4_gemm_kernel<SCHED, PAIR, HALF>, ta, tb, tsa, tsb, p));
 }
 
 template <int SCHED>
@@ -819,10 +816,11 @@ int launch_mxfp4(const Operands &o, MxParams p, cudaStream_t stream) {
     return DG_ERR_CUDA;
   const int sms = effective_num_sms();
   static int per_sm[kMaxDevices] = {};
-  if (per_sm[dev] == 0 && cudaDeviceGetAttribute(&per_sm[dev],
-                                                 cudaDevAttrMaxSharedMemoryPerMultiprocessor,
-                                                 dev) != cudaSuccess)
-    return DG_ERR_CUDA;
+  if (per_sm[dev] == 0) {
+    const int rc = cuda_status(cudaDeviceGetAttribute(
+        &per_sm[dev], cudaDevAttrMaxSharedMemoryPerMultiprocessor, dev));
+    if (rc) return rc;
+  }
   // less the barriers (static), and the kilobyte that the system takes per CTA
   const Smem max = {info->max_smem_optin - 512, per_sm[dev] / 2 - 1024 - 512};
   int rc = configure<SCHED, false, false>(dev, max.full);

@@ -408,7 +408,7 @@ int launch(void (*kern)(P...), dim3 grid, cudaStream_t stream, A... args) {
   cudaLaunchAttribute attr[1] = {pdl_attribute()};
   cfg.attrs = attr;
   cfg.numAttrs = 1;
-  return cudaLaunchKernelEx(&cfg, kern, args...) == cudaSuccess ? DG_OK : DG_ERR_CUDA;
+  return cuda_status(cudaLaunchKernelEx(&cfg, kern, args...));
 }
 
 int check_device() {

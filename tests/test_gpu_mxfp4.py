@@ -8,6 +8,8 @@ of the K/64 + 64 roundings of an element loses at most 2^-23 of the sum S of its
 terms' magnitudes.
 """
 
+import ctypes
+
 import numpy as np
 import pytest
 import torch
@@ -446,6 +448,48 @@ def test_streams_side_by_side():
     torch.cuda.synchronize()
     for d in d1 + d2:
         check(d, a, b)
+    assert dg.dg_get_device_status() == 0
+
+
+def test_a_refused_launch_leaves_no_error_behind():
+    """A launch that CUDA refuses (the default stream while a stream that waits for it
+    is being captured) is that call's error alone."""
+    cudart = ctypes.CDLL("libcudart.so.12")   # torch's, already loaded
+    lib = dg.load_library()
+    x = torch.randn(32, 128, device="cuda")
+    q, sf = dg.dg_quantize_mxfp4(x)
+    d = torch.empty((32, 32), dtype=torch.bfloat16, device="cuda")
+    y = torch.empty_like(x)
+    out = dg.dg_moe_route(x, 4)
+    codes = torch.empty((32, 128), dtype=torch.uint8, device="cuda")
+    scales = torch.empty((1, 32), device="cuda")
+    dlog = dg.dg_moe_route_backward(x, out[0], out[1], out[2], out[4])
+    P = lambda t: t.data_ptr()
+    calls = {
+        "quantize": (lib.dg_quantize_mxfp4, P(x), 0, 1, 32, 128, 128, 0, P(q), P(sf)),
+        "dequantize": (lib.dg_dequantize_mxfp4, P(q), P(sf), 1, 32, 128, P(y), 0, 128),
+        "product": (lib.dg_mxfp4_gemm_nt, P(q), P(sf), P(q), P(sf), P(d), 32, 32, 128),
+        "route": (lib.dg_moe_route, P(x), 0, 32, 128, 128, 4, 1, None, *map(P, out), None, 0),
+        "gradient": (lib.dg_moe_route_backward, P(x), 0, 32, 128, 128, 4, 1, P(out[0]), P(out[1]),
+                     P(out[2]), P(out[4]), None, None, P(dlog)),
+    }
+    for name, (fn, *args) in calls.items():
+        assert fn(*args, None) == dg.DG_OK, name
+    torch.cuda.synchronize()
+    for name, (fn, *args) in calls.items():
+        stream, graph = ctypes.c_void_p(), ctypes.c_void_p()
+        assert cudart.cudaStreamCreate(ctypes.byref(stream)) == 0   # it waits for the default one
+        assert cudart.cudaStreamBeginCapture(stream, 2) == 0        # relaxed
+        rc = fn(*args, None)
+        cudart.cudaStreamEndCapture(stream, ctypes.byref(graph))    # (the capture is void)
+        assert cudart.cudaStreamDestroy(stream) == 0
+        cudart.cudaGetLastError()
+        assert rc == dg.DG_ERR_CUDA, name
+        after = lib.dg_quantize_1x128(P(x), 0, 1, 32, 128, 128, P(codes), 128, P(scales), 32, 0,
+                                      None)
+        assert after == dg.DG_OK, name
+        assert fn(*args, None) == dg.DG_OK, name
+    torch.cuda.synchronize()
     assert dg.dg_get_device_status() == 0
 
 
