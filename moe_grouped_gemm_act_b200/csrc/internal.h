@@ -157,10 +157,11 @@ size_t gemm_workspace_size(int64_t M, int64_t N, int64_t K, int num_sms);
 
 // ---------------------------------------------------------------- device state
 struct DeviceInfo {
-  int ok;            // 1 when the device is usable (sm_100)
+  int ok;              // 1 when the device is usable (sm_100)
   int num_sms;
-  int max_smem_optin;
-  int *status;       // device address of the status word
+  int max_smem_optin;  // shared memory a block may ask for
+  int smem_per_sm;     // what an SM has for all its blocks
+  int *status;         // device address of the status word
 };
 
 // Per-device properties (cached); returns nullptr on a CUDA error.

@@ -15,6 +15,7 @@
 #include <cuda_bf16.h>
 #include <cuda_runtime.h>
 
+#include <atomic>
 #include <cstdint>
 
 #include "dg.h"
@@ -704,11 +705,11 @@ constexpr int kMaxContiguousRows = 2048 * 128;
 
 template <int SCHED, bool PAIR, bool HALF>
 int configure(int dev, int smem) {
-  static bool done[kMaxDevices] = {};
-  if (done[dev]) return DG_OK;
+  static std::atomic<bool> done[kMaxDevices];  // (any thread may be the first)
+  if (done[dev].load(std::memory_order_relaxed)) return DG_OK;
   const int rc = cuda_status(cudaFuncSetAttribute(
       mxfp4_gemm_kernel<SCHED, PAIR, HALF>, cudaFuncAttributeMaxDynamicSharedMemorySize, smem));
-  if (!rc) done[dev] = true;
+  if (!rc) done[dev].store(true, std::memory_order_relaxed);
   return rc;
 }
 
@@ -716,8 +717,9 @@ int configure(int dev, int smem) {
 // at once; asked once per device, kernel and size.
 template <int SCHED, bool PAIR, bool HALF>
 int clusters_fit(int dev, int size, int smem) {
-  static int fit[kMaxDevices][9] = {};  // count + 1; 0 = not asked yet
-  if (fit[dev][size] == 0) {
+  static std::atomic<int> fit[kMaxDevices][9];  // count + 1; 0 = not asked yet
+  int known = fit[dev][size].load(std::memory_order_relaxed);
+  if (known == 0) {
     cudaLaunchConfig_t q = {};
     q.gridDim = dim3(size);
     q.blockDim = dim3(kThreads);
@@ -734,9 +736,10 @@ int clusters_fit(int dev, int size, int smem) {
       cudaGetLastError();
       n = 0;
     }
-    fit[dev][size] = n + 1;
+    known = n + 1;
+    fit[dev][size].store(known, std::memory_order_relaxed);
   }
-  return fit[dev][size] - 1;
+  return known - 1;
 }
 
 // CTAs of a cluster that split K, for `tiles` tiles of one wave.
@@ -815,14 +818,8 @@ int launch_mxfp4(const Operands &o, MxParams p, cudaStream_t stream) {
   if (!info || cudaGetDevice(&dev) != cudaSuccess || dev < 0 || dev >= kMaxDevices)
     return DG_ERR_CUDA;
   const int sms = effective_num_sms();
-  static int per_sm[kMaxDevices] = {};
-  if (per_sm[dev] == 0) {
-    const int rc = cuda_status(cudaDeviceGetAttribute(
-        &per_sm[dev], cudaDevAttrMaxSharedMemoryPerMultiprocessor, dev));
-    if (rc) return rc;
-  }
   // less the barriers (static), and the kilobyte that the system takes per CTA
-  const Smem max = {info->max_smem_optin - 512, per_sm[dev] / 2 - 1024 - 512};
+  const Smem max = {info->max_smem_optin - 512, info->smem_per_sm / 2 - 1024 - 512};
   int rc = configure<SCHED, false, false>(dev, max.full);
   if (!rc && SCHED != kMxContiguous)
     rc = configure<SCHED, false, SCHED != kMxContiguous>(dev, max.half);

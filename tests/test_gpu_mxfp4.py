@@ -9,6 +9,9 @@ terms' magnitudes.
 """
 
 import ctypes
+import os
+import subprocess
+import sys
 
 import numpy as np
 import pytest
@@ -449,6 +452,59 @@ def test_streams_side_by_side():
     for d in d1 + d2:
         check(d, a, b)
     assert dg.dg_get_device_status() == 0
+
+
+FIRST_CALLS = """
+import threading, torch
+import moe_grouped_gemm_act_b200 as dg
+
+gen = torch.Generator(device="cuda").manual_seed(5)
+def operand(*shape):
+    return dg.dg_quantize_mxfp4(torch.randn(*shape, device="cuda", generator=gen))
+# one product for each form: K split, two CTAs per SM, CTA pairs, single CTAs
+dense = [(operand(m, k), operand(n, k)) for m, n, k in
+         [(5, 256, 2048), (17, 20000, 96), (2500, 2008, 160), (300, 200, 224)]]
+masked = [(operand(4, m, 160), operand(4, 264, 160)) for m in (40, 300)]
+mm = torch.tensor([1, 0, 40, 17], dtype=torch.int32, device="cuda")
+cont = [(operand(m, 160), operand(2, 4872, 160)) for m in (256, 4096)]
+new = lambda *shape: torch.zeros(shape, dtype=torch.bfloat16, device="cuda")
+torch.cuda.synchronize()
+
+def run():
+    out = []
+    for (a, sa), (b, sb) in dense:
+        out.append(dg.dg_mxfp4_gemm_nt(a, sa, b, sb, new(len(a), len(b))))
+    for (a, sa), (b, sb) in masked:
+        out.append(dg.dg_m_grouped_mxfp4_gemm_nt_masked(a, sa, b, sb, new(4, a.shape[1], 264), mm))
+    for (a, sa), (b, sb) in cont:
+        idx = torch.arange(len(a), device="cuda", dtype=torch.int32) // 128 % 2
+        out.append(dg.dg_m_grouped_mxfp4_gemm_nt_contiguous(a, sa, b, sb, new(len(a), 4872), idx))
+    return out
+
+start, got = threading.Barrier(4), {}
+def work(i):
+    with torch.cuda.stream(torch.cuda.Stream()):
+        start.wait()
+        got[i] = run()
+        torch.cuda.current_stream().synchronize()
+threads = [threading.Thread(target=work, args=(i,)) for i in range(4)]
+[t.start() for t in threads]
+[t.join() for t in threads]
+want = run()
+torch.cuda.synchronize()
+assert sorted(got) == [0, 1, 2, 3]
+assert all(torch.equal(u, v) for g in got.values() for u, v in zip(g, want))
+assert dg.dg_get_device_status() == 0
+"""
+
+
+def test_first_calls_from_several_threads():
+    """What the library asks of a device once, asked by four threads at once (in a
+    process of its own, where no product has run)."""
+    root = os.path.dirname(os.path.dirname(os.path.abspath(__file__)))
+    r = subprocess.run([sys.executable, "-c", FIRST_CALLS], cwd=root, capture_output=True,
+                       text=True, timeout=600)
+    assert r.returncode == 0, r.stdout + r.stderr
 
 
 def test_a_refused_launch_leaves_no_error_behind():
