@@ -46,13 +46,8 @@ constexpr uint32_t kSfBBytes = kStageWords * kMxBlockBytes;     // one row block
 constexpr uint32_t kSfSlotCols = 32;
 constexpr int kSfSlots = 4;
 // A CTA takes a whole SM (512 columns) or, with tiles of up to 64 tokens, half
-// of one (256 columns, half the registers and shared memory).  The shared
-// memory of a whole one stays above half an SM's, so that no two CTAs that
-// together want more than the 512 columns sit on one SM: a CTA of a cluster
-// that waits for TMEM there while its peers wait for it could deadlock two
-// launches.
+// of one (256 columns, half the registers and shared memory): smem_apart.
 constexpr int kHalfTokens = 64;
-constexpr int kMinSmem = 120 * 1024;
 
 struct MxParams {
   uint16_t *d;
@@ -766,25 +761,66 @@ struct Operands {
   const int32_t *sfa, *sfb;
 };
 
-// Fills in the shapes that follow from p and launches `grid` CTAs.
-// Dynamic shared memory that a CTA may take: all of an SM's, or half.
+// Dynamic shared memory that a CTA may take: all of an SM's, or half -- less the
+// barriers (static) and, twice in a half, the kilobyte that the system takes per CTA.
 struct Smem {
-  int full, half;
+  int full, half, per_sm;
 };
+constexpr Smem smem_limits(int optin, int per_sm) {
+  return {optin - 512, per_sm / 2 - 1024 - 512, per_sm};
+}
 
+// The ring of a form: the stages that fit beside `tables` bytes of tables, and
+// the shared memory that they make.
+struct RingSize {
+  int stages, smem;
+};
+constexpr RingSize ring_of(bool pair, bool half, int tok_tile, int tables, const Smem &max) {
+  const int stage = static_cast<int>(kBBytes) + (pair ? tok_tile / 2 : tok_tile) * (kStageK / 2) +
+                    static_cast<int>(kSfBBytes) * (tok_tile > 128 ? 3 : 2);
+  const int besides = 1024 + kEpiWarps * kTurnBytes + tables;
+  const int fit = ((half ? max.half : max.full) - besides) / stage;
+  const int stages = fit < kMaxStages ? fit : kMaxStages;
+  return {stages, besides + stages * stage};
+}
+
+// TMEM is taken before the dependency wait, and the next launch starts before that:
+// if CTAs that together want more than an SM's 512 columns met on one, one that
+// waits for its columns (in a cluster, with its peers waiting for it) and one that
+// holds them and waits for the launch before it would wait for each other.
+// Shared memory keeps them apart: a whole SM's CTA takes more than two thirds of
+// it, half an SM's more than a third, so a second one beside the first or a third
+// beside two halves does not fit.  (The library's FP8 kernels, with 144 KB and more,
+// do not fit beside the smallest half either, 87 KB of 228.)
+constexpr bool smem_apart(bool half, int smem, int per_sm) {
+  return 3 * smem > (half ? 1 : 2) * per_sm;
+}
+constexpr int kMaxGroups = 1024;  // of the masked form
+constexpr bool all_apart(const Smem &max) {
+  for (int tables : {0, (kMaxGroups + 1) * 4, kMaxContiguousRows / 128 * 8})
+    for (int t = 16; t <= kMaxTokens; t *= 2) {
+      if (!smem_apart(false, ring_of(false, false, t, tables, max).smem, max.per_sm)) return false;
+      if (t == kMaxTokens &&
+          !smem_apart(false, ring_of(true, false, t, tables, max).smem, max.per_sm))
+        return false;
+      if (t <= kHalfTokens && tables <= (kMaxGroups + 1) * 4 &&
+          !smem_apart(true, ring_of(false, true, t, tables, max).smem, max.per_sm))
+        return false;
+    }
+  return true;
+}
+static_assert(all_apart(smem_limits(227 * 1024, 228 * 1024)), "a B200's SM");
+
+// Fills in the shapes that follow from p and launches `grid` CTAs.
 template <int SCHED, bool PAIR, bool HALF>
 int launch_form(const Operands &o, MxParams p, int grid, const Smem &max, cudaStream_t stream) {
   const int a_rows = PAIR ? p.tok_tile / 2 : p.tok_tile;
-  const int stage = static_cast<int>(kBBytes) + a_rows * (kStageK / 2) +
-                    static_cast<int>(kSfBBytes) * (p.tok_tile > 128 ? 3 : 2);
-  const int besides = 1024 + kEpiWarps * kTurnBytes +
-                      (SCHED == kMxMasked       ? (p.groups + 1) * 4
-                       : SCHED == kMxContiguous ? p.rows / 128 * 8
-                                                : 0);
-  p.stages = ((HALF ? max.half : max.full) - besides) / stage;
-  if (p.stages > kMaxStages) p.stages = kMaxStages;
-  int smem = besides + p.stages * stage;
-  if (!HALF && smem < kMinSmem) smem = kMinSmem;
+  const int tables = SCHED == kMxMasked       ? (p.groups + 1) * 4
+                     : SCHED == kMxContiguous ? p.rows / 128 * 8
+                                              : 0;
+  const RingSize ring = ring_of(PAIR, HALF, p.tok_tile, tables, max);
+  if (!smem_apart(HALF, ring.smem, max.per_sm)) return DG_ERR_UNSUPPORTED_ARCH;
+  p.stages = ring.stages;
   CUtensorMap ta, tb, tsa, tsb;
   const int slabs = SCHED == kMxMasked ? p.groups : 1;
   int rc = make_tmap(&ta, o.a, p.k, p.rows, slabs, a_rows);
@@ -797,7 +833,7 @@ int launch_form(const Operands &o, MxParams p, int grid, const Smem &max, cudaSt
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = dim3(grid);
   cfg.blockDim = dim3(kThreads);
-  cfg.dynamicSmemBytes = smem;
+  cfg.dynamicSmemBytes = ring.smem;
   cfg.stream = stream;
   cudaLaunchAttribute attr[2];
   attr[0] = pdl_attribute();
@@ -818,8 +854,7 @@ int launch_mxfp4(const Operands &o, MxParams p, cudaStream_t stream) {
   if (!info || cudaGetDevice(&dev) != cudaSuccess || dev < 0 || dev >= kMaxDevices)
     return DG_ERR_CUDA;
   const int sms = effective_num_sms();
-  // less the barriers (static), and the kilobyte that the system takes per CTA
-  const Smem max = {info->max_smem_optin - 512, info->smem_per_sm / 2 - 1024 - 512};
+  const Smem max = smem_limits(info->max_smem_optin, info->smem_per_sm);
   int rc = configure<SCHED, false, false>(dev, max.full);
   if (!rc && SCHED != kMxContiguous)
     rc = configure<SCHED, false, SCHED != kMxContiguous>(dev, max.half);
@@ -960,7 +995,7 @@ extern "C" int dg_m_grouped_mxfp4_gemm_nt_masked(const uint8_t *A, const int32_t
                                                  const int32_t *masked_m, int G, int64_t M_max,
                                                  int64_t N, int64_t K, dg_stream_t stream) {
   using namespace dg;
-  if (G < 1 || G > 1024 || M_max < 1) return DG_ERR_INVALID_ARG;
+  if (G < 1 || G > kMaxGroups || M_max < 1) return DG_ERR_INVALID_ARG;
   int rc = check_gemm(A, sfa, B, sfb, D, M_max, N, K, G, G);
   if (rc) return rc;
   if (!masked_m) return DG_ERR_INVALID_ARG;
