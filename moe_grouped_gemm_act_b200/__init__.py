@@ -42,6 +42,12 @@ Entry points (same names as the C ABI):
   ``dg_get_mk_alignment_for_contiguous_layout``, ``dg_set_num_sms``,
   ``dg_get_num_sms``, ``dg_fp8_gemm_nt_workspace_size``.
 
+``stream`` (a ``torch.cuda.Stream``; the current one if not given) is where a call
+runs.  It does not wait for other streams: what its inputs hold must be ready
+there.  The MXFP4 and routing calls mark their tensors as used on a stream that
+is given, so temporaries may be passed; for the other calls keep the tensors until
+the stream is done with them (or call ``record_stream``).
+
 Layouts follow the header: A [M, K] uint8 (E4M3 codes), its scales MN-major
 [K/128, ld] (``sf.t()`` of the logical [M, K/128]), B [N, K] uint8 with scales
 [ceil(N/128), K/128], D [M, N] bfloat16.
@@ -684,6 +690,10 @@ def _on_device(name, fn_args, ts, stream):
             rc = fn(*fn_args, raw)
     if rc != DG_OK:
         raise DGError(rc, name)
+    if stream is not None:
+        # the caller may drop a tensor while the stream still uses it
+        for t in ts:
+            t.record_stream(stream)
 
 
 def _exact(t, name, dtype, shape):

@@ -336,6 +336,31 @@ def test_two_streams_at_once():
         assert all(torch.equal(u, v) for u, v in zip(a, b))
 
 
+def test_temporaries_with_a_given_stream():
+    """A mask and logits that are dropped right after the call, while the stream that
+    was given has not come to it yet: their memory is not handed out before."""
+    t, e, k = 70000, 40, 4
+    xd, x = logits(200, e, 79)
+    xd = xd.repeat(t // 200, 1)
+    keep = torch.arange(t, device="cuda") % 3 > 0
+    want = dg.dg_moe_route(xd, k, token_mask=keep)
+    side = torch.cuda.Stream()
+    torch.cuda.synchronize()
+    for _ in range(3):
+        with torch.cuda.stream(side):
+            torch.cuda._sleep(20_000_000)             # some 10 ms
+        temps = xd + 0.0, keep.clone()
+        torch.cuda.current_stream().synchronize()     # (they are ready)
+        got = dg.dg_moe_route(temps[0], k, token_mask=temps[1], stream=side)
+        del temps
+        refill = [torch.full((t,), False, device="cuda"),
+                  torch.full((t, e), float("nan"), device="cuda")]
+        torch.cuda.synchronize()
+        assert all(torch.equal(a, b) for a, b in zip(got, want))
+        del refill
+    assert dg.dg_get_device_status() == 0
+
+
 def test_a_layer_of_experts():
     """Routing, the experts' MXFP4 products on both layouts, and the weighted sum:
     counts feed masked_m, and the two layouts give the same rows."""

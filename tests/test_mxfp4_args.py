@@ -162,3 +162,35 @@ def test_route_workspace_size_of_refused_experts():
     assert set(eval(r.stdout)) == {0}
     for e in (1, 1024):
         assert dg.dg_moe_route_workspace_size(257, e) > 0
+
+
+class _OnStream:
+    """What the binding asks of a tensor on cuda:0."""
+    device = torch.device("cuda", 0)
+
+    def __init__(self):
+        self.used_on = []
+
+    def get_device(self):
+        return 0
+
+    def record_stream(self, stream):
+        self.used_on.append(stream)
+
+
+def test_tensors_are_marked_as_used_on_a_given_stream(monkeypatch):
+    """A temporary passed with stream= is not handed out again while the stream still
+    reads it."""
+    class Stream:
+        device, cuda_stream = torch.device("cuda", 0), 7
+
+    calls = []
+    monkeypatch.setattr(torch._C, "_cuda_getDevice", lambda: 0)
+    monkeypatch.setattr(torch._C, "_cuda_getCurrentRawStream", lambda dev: 3)
+    monkeypatch.setattr(dg, "_lib", type("Lib", (), {
+        "entry": staticmethod(lambda *a: calls.append(a) or OK)}))
+    s, ts = Stream(), [_OnStream(), _OnStream()]
+    dg._on_device("entry", (1,), ts, None)
+    assert calls == [(1, 3)] and all(t.used_on == [] for t in ts)
+    dg._on_device("entry", (2,), ts, s)
+    assert calls[1] == (2, 7) and all(t.used_on == [s] for t in ts)
