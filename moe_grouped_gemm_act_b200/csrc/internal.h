@@ -155,6 +155,18 @@ int launch_fp8_gemm(int sched, const uint8_t *A, const uint8_t *B,
 
 size_t gemm_workspace_size(int64_t M, int64_t N, int64_t K, int num_sms);
 
+// ---------------------------------------------------------------- test knobs
+// Of the abort path, both unset in normal use: DG_TEST_STARVE_LOAD=i makes CTA 0's
+// producer leave out the loads of its iteration i (a kernel parameter, -1: none);
+// DG_TEST_WAIT_LIMIT_US=t lowers every wait's limit to t microseconds (at least
+// kWaitCheckNs), written to the device before the call's kernel and put back after
+// it, in stream order.
+struct TestKnobs {
+  int starve = -1;
+  unsigned long long limit_ns = 0;  // 0: the limit as it is
+};
+TestKnobs test_knobs();
+
 // ---------------------------------------------------------------- device state
 struct DeviceInfo {
   int ok;              // 1 when the device is usable (sm_100)

@@ -61,6 +61,7 @@ struct MxParams {
   int n_tiles;       // ceil(n / 128), for the pair form ceil(n / 256)
   int stages;
   int splits;        // CTAs of a cluster that split a tile's K (dense; 1: none)
+  int starve;        // test hook: the stage whose loads CTA 0 leaves out (-1: none)
 };
 
 struct Tile {
@@ -373,6 +374,8 @@ mxfp4_gemm_kernel(const __grid_constant__ CUtensorMap tmap_a,
     if (elect_one()) {
     Ring ring;
     int issued = 0;  // stages, counted up to the ring's length
+    int it = 0;
+    const int starve = blockIdx.x == 0 ? p.starve : -1;
     for_each_tile<SCHED, PAIR>(p, tab, [&](const Tile &t) {
       const int b_block = t.group * b_blocks + t.n0 / 128;
       const int a_block = t.slab * a_blocks + t.tok0 / 128;
@@ -380,7 +383,7 @@ mxfp4_gemm_kernel(const __grid_constant__ CUtensorMap tmap_a,
       for (int ks = t.k_begin; ks < t.k_end; ++ks) {
         const int s = ring.slot;
         if (!mbar_wait(empty_bar(s), ring.parity ^ 1, abort, p.status)) return false;
-        {
+        if (it != starve) {
           const uint32_t sb = base + static_cast<uint32_t>(s) * stage_bytes;
           const uint32_t sf = sf_base + static_cast<uint32_t>(s) * sf_stage;
           const int kc = ks * (kStageK / 2), wc = ks * kStageWords;
@@ -402,6 +405,7 @@ mxfp4_gemm_kernel(const __grid_constant__ CUtensorMap tmap_a,
         }
         ring.advance(p.stages);
         if (issued < p.stages) ++issued;
+        ++it;
       }
       return true;
     });
@@ -413,8 +417,9 @@ mxfp4_gemm_kernel(const __grid_constant__ CUtensorMap tmap_a,
     if (rank == 0)
       for (int i = 0; i < issued; ++i) {
         // slots before the ring's place were used with its parity, the others
-        // with the one before
-        mbar_wait(full_bar(i), i < ring.slot ? ring.parity : ring.parity ^ 1, &never, p.status);
+        // with the one before (a stage that was left out has no copies)
+        if (starve < 0 || it <= starve || i != starve % p.stages)
+          mbar_wait(full_bar(i), i < ring.slot ? ring.parity : ring.parity ^ 1, &never, p.status);
       }
     }
     __syncwarp();
@@ -848,7 +853,7 @@ int launch_form(const Operands &o, MxParams p, int grid, const Smem &max, cudaSt
 }
 
 template <int SCHED>
-int launch_mxfp4(const Operands &o, MxParams p, cudaStream_t stream) {
+int launch_forms(const Operands &o, MxParams p, cudaStream_t stream) {
   const DeviceInfo *info = device_info();
   int dev = 0;
   if (!info || cudaGetDevice(&dev) != cudaSuccess || dev < 0 || dev >= kMaxDevices)
@@ -910,6 +915,18 @@ int launch_mxfp4(const Operands &o, MxParams p, cudaStream_t stream) {
       return launch_form<SCHED, false, false>(o, p, sms, max, stream);
     }
   }
+}
+
+template <int SCHED>
+int launch_mxfp4(const Operands &o, MxParams p, cudaStream_t stream) {
+  const TestKnobs knobs = test_knobs();
+  p.starve = knobs.starve;
+  if (knobs.limit_ns == 0) return launch_forms<SCHED>(o, p, stream);
+  int rc = cuda_status(set_wait_limit(knobs.limit_ns, stream));
+  if (rc) return rc;
+  rc = launch_forms<SCHED>(o, p, stream);
+  const int rc2 = cuda_status(set_wait_limit(kWaitLimitNs, stream));
+  return rc ? rc : rc2;
 }
 
 int check_gemm(const void *A, const void *sfa, const void *B, const void *sfb, const void *D,

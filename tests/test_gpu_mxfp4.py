@@ -8,6 +8,7 @@ of the K/64 + 64 roundings of an element loses at most 2^-23 of the sum S of its
 terms' magnitudes.
 """
 
+import contextlib
 import ctypes
 import os
 import subprocess
@@ -451,6 +452,78 @@ def test_streams_side_by_side():
     torch.cuda.synchronize()
     for d in d1 + d2:
         check(d, a, b)
+    assert dg.dg_get_device_status() == 0
+
+
+@contextlib.contextmanager
+def starved(stage):
+    """CTA 0 leaves out the loads of its `stage`-th stage; waits run out after 20 ms."""
+    names = {"DG_TEST_STARVE_LOAD": str(stage), "DG_TEST_WAIT_LIMIT_US": "20000"}
+    os.environ.update(names)
+    try:
+        yield
+    finally:
+        for name in names:
+            del os.environ[name]
+
+
+@pytest.mark.parametrize("stage", [0, 2])
+@pytest.mark.parametrize("m,n,k", [
+    (5, 256, 2048),         # K split over a cluster (one stage for each CTA: stage 0 alone)
+    (5, 256, 7168),         # the same, several stages each
+    (17, 20000, 1312),      # two CTAs per SM
+    (100, 20000, 1056),     # single CTAs
+    (2500, 2008, 3328)])    # CTA pairs
+def test_lost_load_times_out_and_the_next_product_is_right(m, n, k, stage):
+    """Nothing completes a stage that was left out: the bounded waits run out, the CTAs
+    leave after the copies that are still in flight, and the call reports it."""
+    qa, sa, a = random_operand(m, k, 6)
+    qb, sb, b = random_operand(n, k, 7)
+    d = torch.empty((m, n), dtype=torch.bfloat16, device="cuda")
+    dg.dg_get_device_status()
+    with starved(stage):
+        dg.dg_mxfp4_gemm_nt(qa, sa, qb, sb, d)
+        torch.cuda.synchronize()
+    lost = stage == 0 or k != 2048
+    assert dg.dg_get_device_status() == (dg.DG_ERR_TIMEOUT if lost else 0)
+    for _ in range(2):
+        d.view(torch.int16).fill_(SENTINEL)
+        dg.dg_mxfp4_gemm_nt(qa, sa, qb, sb, d)
+        check(d, a.double(), b.double())
+    assert dg.dg_get_device_status() == 0
+
+
+@pytest.mark.parametrize("m,n", [(256, 264), (4096, 4872)])
+def test_lost_load_of_grouped_products(m, n):
+    """The contiguous and the masked form, single CTAs and CTA pairs (masked: also two
+    CTAs per SM)."""
+    k, g = 1056, 2
+    qb, sb = (torch.stack(t) for t in zip(*(random_operand(n, k, s)[:2] for s in (1, 2))))
+    b = [random_operand(n, k, s)[2].double() for s in (1, 2)]
+    qa, sa, a = random_operand(m, k, 3)
+    idx = torch.arange(m, device="cuda", dtype=torch.int32) // (m // 2)
+    d = torch.empty((m, n), dtype=torch.bfloat16, device="cuda")
+    with starved(1):
+        dg.dg_m_grouped_mxfp4_gemm_nt_contiguous(qa, sa, qb, sb, d, idx)
+        torch.cuda.synchronize()
+    assert dg.dg_get_device_status() == dg.DG_ERR_TIMEOUT
+    dg.dg_m_grouped_mxfp4_gemm_nt_contiguous(qa, sa, qb, sb, d, idx)
+    for e in range(g):
+        check(d[idx == e], a[idx == e].double(), b[e])
+    for m_max, groups in ((40, 64), (100, 2), (256, 2)):   # (64 experts' tiles outnumber the SMs)
+        ops = [random_operand(m_max, k, 10 + e) for e in range(groups)]
+        qm, sm = (torch.stack(t) for t in zip(*(o[:2] for o in ops)))
+        rep = lambda t: t.repeat(groups // g, *[1] * (t.dim() - 1))
+        mm = torch.full((groups,), m_max, dtype=torch.int32, device="cuda")
+        dm = torch.empty((groups, m_max, n), dtype=torch.bfloat16, device="cuda")
+        args = (qm, sm, rep(qb), rep(sb), dm, mm)
+        with starved(1):
+            dg.dg_m_grouped_mxfp4_gemm_nt_masked(*args)
+            torch.cuda.synchronize()
+        assert dg.dg_get_device_status() == dg.DG_ERR_TIMEOUT
+        dg.dg_m_grouped_mxfp4_gemm_nt_masked(*args)
+        for e in range(groups):
+            check(dm[e], ops[e][2].double(), b[e % g])
     assert dg.dg_get_device_status() == 0
 
 
