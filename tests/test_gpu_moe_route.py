@@ -188,6 +188,43 @@ def test_strided_logits(dtype):
         assert torch.equal(ga, gb)
 
 
+@pytest.mark.parametrize("dtype", [torch.float32, torch.bfloat16])
+def test_offsets_past_32_bits(dtype):
+    """Rows so far apart that the last ones lie past 2^32 bytes and 2^31 elements."""
+    t, e, ld = 40000, 60, 1 << 16
+    base = torch.empty((t, ld), dtype=dtype, device="cuda")
+    x = base[:, 4:4 + e]
+    x.copy_(torch.randn(t, e, device="cuda"))
+    a, b = dg.dg_moe_route(x, 4), dg.dg_moe_route(x.contiguous(), 4)
+    assert all(torch.equal(u, v) for u, v in zip(a, b))
+    dw = torch.randn(t, 4, device="cuda")
+    ga = dg.dg_moe_route_backward(x, a[0], a[1], a[2], a[4], dw, a[3])
+    gb = dg.dg_moe_route_backward(x.contiguous(), a[0], a[1], a[2], a[4], dw, a[3])
+    assert torch.equal(ga, gb)
+
+
+def test_padded_batch_with_garbage():
+    """A padded batch: what the left-out tokens hold (NaN, infinities) in logits and in
+    the incoming gradient reaches nothing."""
+    t, e, k = 700, 72, 6
+    xd, x = logits(t, e, 80)
+    mask = np.random.default_rng(2).random(t) < 0.7
+    md = dev(mask)
+    xd[~md] = torch.tensor([np.nan, np.inf, -np.inf] * (e // 3), device="cuda")
+    x[~mask] = 0.0
+    for normalize in (True, False):
+        out = dg.dg_moe_route(xd, k, normalize, md)
+        oi, ow, oc, on, p = check_forward(out, x, k, normalize, mask)
+        dw = np.random.default_rng(3).normal(size=(t, k)).astype(np.float32)
+        dwd = dev(dw)
+        dwd[~md] = float("nan")
+        d = dg.dg_moe_route_backward(xd, *(out[i] for i in (0, 1, 2, 4)), dwd,
+                                     torch.full((1,), 0.5, device="cuda"), normalize)
+        check_backward(d, x, p, oi, ow, oc, on, dw, 0.5, normalize, False)
+        assert bool((d[~md] == 0).all())
+    assert dg.dg_get_device_status() == 0
+
+
 def test_gradient_against_differences():
     """The kernels' own weights and loss, in differences of the logits."""
     t, e, k = 12, 16, 3
@@ -322,6 +359,34 @@ def test_graph_replay_and_two_graphs():
         want = (*o, dg.dg_moe_route_backward(x, o[0], o[1], o[2], o[4], o[1], o[3]))
         for got in outs:
             assert all(torch.equal(a, b) for a, b in zip(got, want))
+
+
+def test_captured_on_a_forked_stream():
+    """A graph whose calls are given a stream that forks from the captured one."""
+    t, e, k = 900, 40, 3
+    xs = [logits(t, e, s)[0] for s in (81, 82)]
+    side = torch.cuda.Stream()
+    dg.dg_moe_route(xs[0], k)
+    buf = xs[0].clone()
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        temp = buf[:, :32].contiguous()
+        side.wait_stream(torch.cuda.current_stream())
+        out = dg.dg_moe_route(buf, k, stream=side)
+        dlog = dg.dg_moe_route_backward(buf, out[0], out[1], out[2], out[4], out[1], out[3],
+                                        stream=side)
+        q, sf = dg.dg_quantize_mxfp4(temp, stream=side)
+        del temp                          # (and its memory must not serve the next line)
+        other = torch.full((t, 32), float("nan"), device="cuda")
+        torch.cuda.current_stream().wait_stream(side)
+    for x in (xs[1], xs[0]):
+        buf.copy_(x)
+        graph.replay()
+        torch.cuda.synchronize()
+        o = dg.dg_moe_route(x, k)
+        want = (*o, dg.dg_moe_route_backward(x, o[0], o[1], o[2], o[4], o[1], o[3]),
+                *dg.dg_quantize_mxfp4(x[:, :32].contiguous()))
+        assert all(torch.equal(a, b) for a, b in zip((*out, dlog, q, sf), want))
 
 
 def test_two_streams_at_once():

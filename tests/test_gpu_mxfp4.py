@@ -159,6 +159,51 @@ def test_quantize_batch_and_empty():
     assert q.shape == (0, 32) and dg.dg_dequantize_mxfp4(q, sf).shape == (0, 64)
 
 
+@pytest.mark.parametrize("batch,m", [(70000, 2), (1, 600000)])
+def test_quantize_past_the_grid(batch, m):
+    """More matrices and more rows than a grid has blocks for."""
+    k = 32
+    x = torch.randn(batch, m, k, device="cuda")
+    q, sf = dg.dg_quantize_mxfp4(x)
+    y = dg.dg_dequantize_mxfp4(q, sf, torch.float32)
+    for i in (0, 1, 65535, 65536, 524287, 524288, batch * m - 1):
+        b, r = divmod(i, m)
+        if b < batch:
+            codes, byte = mxfp4.quantize(x[b, r:r + 1].cpu().numpy())
+            assert np.array_equal(q[b, r:r + 1].cpu().numpy(), mxfp4.pack(codes))
+            assert np.array_equal(y[b, r:r + 1].cpu().numpy(), mxfp4.values(codes, byte))
+    # the worst element is 5 2^e, halfway between 4 and 6: a fifth of it, and so of amax at most
+    assert bool(((y - x).abs() <= 0.2001 * x.abs().amax(-1, keepdim=True)).all())
+
+
+def test_quantize_columns_past_the_grid():
+    k, m = 65536 * 256 + 96, 3
+    x = torch.randn(k, m, device="cuda").to(torch.bfloat16)
+    q, sf = dg.dg_quantize_mxfp4(x, transpose=True)
+    for at in (0, 65535 * 256, k - 96):
+        codes, byte = mxfp4.quantize(x[at:at + 96].float().cpu().numpy().T.copy())
+        assert np.array_equal(q[:, at // 2:at // 2 + 48].cpu().numpy(), mxfp4.pack(codes))
+    y = dg.dg_dequantize_mxfp4(q, sf)
+    assert bool(((y.t().float() - x.float()).abs() <=
+                 0.2001 * x.float().view(-1, 32, m).abs().amax(1).repeat_interleave(32, 0)).all())
+
+
+@pytest.mark.parametrize("dtype", [torch.float32, torch.bfloat16])
+def test_read_back_into_wider_rows(dtype):
+    """The C call's row stride: what lies past K stays."""
+    m, k, ld = 37, 96, 136
+    codes, byte = mxfp4.quantize(rnd((m, k), 8))
+    q, sf = dev(mxfp4.pack(codes)), dev(mxfp4.scale_words(byte))
+    y = torch.full((m + 1, ld), -3.0, dtype=dtype, device="cuda")
+    rc = dg.load_library().dg_dequantize_mxfp4(
+        q.data_ptr(), sf.data_ptr(), 1, m, k, y.data_ptr(),
+        dg.DG_DTYPE_F32 if dtype == torch.float32 else dg.DG_DTYPE_BF16, ld,
+        torch.cuda.current_stream().cuda_stream)
+    assert rc == dg.DG_OK
+    assert np.array_equal(y[:m, :k].double().cpu().numpy(), mxfp4.values(codes, byte))
+    assert bool((y[:m, k:] == -3).all()) and bool((y[m] == -3).all())
+
+
 # ------------------------------------------------------------------ dense product
 @pytest.mark.parametrize("m,n,k", [
     (1, 8, 32), (1, 2112, 7168), (2, 136, 96), (5, 128, 128), (16, 256, 288), (17, 1000, 544),
@@ -233,6 +278,32 @@ def test_overlapping_launches_are_ordered():
         graph.replay()
         torch.cuda.synchronize()
         assert torch.equal(copy, want[1])
+
+
+def test_quantizer_behind_a_running_product():
+    """A quantizer that overwrites a product's operands directly behind it, with nothing
+    between the two on the stream: it must not start on them before the product is
+    done; nor a product on what the quantizer has not written yet."""
+    m, n, k = 2500, 2008, 3328
+    qb, sb, b = random_operand(n, k, 3)
+    xs = [torch.randn(m, k, device="cuda") for _ in range(4)]
+    q = torch.empty((m, k // 2), dtype=torch.uint8, device="cuda")
+    sf = torch.empty((20, 26, 32, 4), dtype=torch.int32, device="cuda")
+    new = lambda rows: [torch.empty((rows, n), dtype=torch.bfloat16, device="cuda") for _ in xs]
+    for rows in (m, 100, 5):      # CTA pairs; K split, for the first rows
+        want, got = new(rows), new(rows)
+        blocks = -(-rows // 128)
+        ops = (q[:rows], sf[:blocks], qb, sb)
+        for x, d in zip(xs, want):
+            dg.dg_quantize_mxfp4(x, q=q, sf=sf)
+            torch.cuda.synchronize()
+            dg.dg_mxfp4_gemm_nt(*ops, d)
+            torch.cuda.synchronize()
+        for _ in range(5):
+            for x, d in zip(xs, got):
+                dg.dg_quantize_mxfp4(x, q=q, sf=sf)
+                dg.dg_mxfp4_gemm_nt(*ops, d)
+            assert all(torch.equal(u, v) for u, v in zip(got, want)), rows
 
 
 def test_offsets_past_32_bits():
@@ -320,6 +391,36 @@ def test_gemm_zero_rows_and_sm_cap():
         dg.dg_set_num_sms(0)
 
 
+@pytest.mark.parametrize("cap", [1, 2, 7, 60, 147])
+def test_every_form_under_an_sm_cap(cap):
+    """Pairs, tiles past one per SM, K split, and the grouped forms, on fewer SMs."""
+    cases = [(2500, 1032, 800), (17, 20000, 96), (5, 256, 2048)]
+    ops = [(random_operand(m, k, 1), random_operand(n, k, 2)) for m, n, k in cases]
+    counts = np.array([130, 0, 300, 5], np.int32)
+    idx, qc, sc, ac, qb, sb, b = contiguous(counts, 392, 160, 31)
+    qm, sm, am = operand(rnd((4, 300, 160), 32))
+    try:
+        dg.dg_set_num_sms(cap)
+        for (qa, sa, a), (qw, sw, w) in ops:
+            d = torch.empty((len(a), len(w)), dtype=torch.bfloat16, device="cuda")
+            dg.dg_mxfp4_gemm_nt(qa, sa, qw, sw, d)
+            check(d, a.double(), w.double(), f"cap {cap}")
+        dc = sentinel(len(idx), 392)
+        dg.dg_m_grouped_mxfp4_gemm_nt_contiguous(qc, sc, qb, sb, dc, dev(idx))
+        dm = sentinel(4, 300, 392)
+        dg.dg_m_grouped_mxfp4_gemm_nt_masked(qm, sm, qb, sb, dm, dev(counts))
+    finally:
+        dg.dg_set_num_sms(0)
+    assert untouched(dc[torch.from_numpy(idx < 0).cuda()])
+    for e, c in enumerate(counts):
+        if c:
+            rows = torch.from_numpy(np.flatnonzero(idx == e)).cuda()
+            check(dc[rows], ac[rows], b[e], f"contiguous, cap {cap}")
+            check(dm[e, :c], am[e, :c], b[e], f"masked, cap {cap}")
+        assert untouched(dm[e, c:])
+    assert dg.dg_get_device_status() == 0
+
+
 # ------------------------------------------------------------------ grouped products
 def contiguous(counts, n, k, seed, extra=0):
     idx = []
@@ -405,6 +506,44 @@ def test_masked(counts, m_max, n, k):
         if c:
             check(d[e, :c], a[e, :c], b[e], f"expert {e}")
         assert untouched(d[e, c:])
+    assert dg.dg_get_device_status() == 0
+
+
+@pytest.mark.parametrize("m_max,n", [(8, 72), (130, 40), (300, 264)])
+def test_masked_1024_experts(m_max, n):
+    """The largest table of tiles, most experts empty."""
+    g, k = 1024, 96
+    gen = torch.Generator(device="cuda").manual_seed(n)
+    qa = torch.randint(0, 256, (g, m_max, k // 2), generator=gen, device="cuda", dtype=torch.uint8)
+    qb = torch.randint(0, 256, (g, n, k // 2), generator=gen, device="cuda", dtype=torch.uint8)
+    # unit scales, zero bytes for the group past K
+    one = lambda r: torch.full((g, -(-r // 128), 1, 32, 4), 0x7F7F7F, dtype=torch.int32, device="cuda")
+    val = lambda q: dev(mxfp4.VALUES)[torch.stack([q & 15, q >> 4], -1).flatten(-2).long()]
+    counts = np.random.default_rng(n).integers(0, m_max + 1, g).astype(np.int32)
+    counts[np.random.default_rng(1).random(g) < 0.6] = 0
+    counts[[0, 31, 32, 1023]] = m_max, 0, 1, m_max
+    d = sentinel(g, m_max, n)
+    dg.dg_m_grouped_mxfp4_gemm_nt_masked(qa, one(m_max), qb, one(n), d, dev(counts))
+    live = torch.arange(m_max, device="cuda") < dev(counts)[:, None]
+    assert untouched(d[~live])
+    for e in np.flatnonzero(counts):
+        c = int(counts[e])
+        want = val(qa[e, :c]) @ val(qb[e]).T       # whole quarters below 2^24: exact in FP32
+        assert torch.equal(d[e, :c], want.float().to(torch.bfloat16)), e
+    assert dg.dg_get_device_status() == 0
+
+
+def test_contiguous_many_experts():
+    g, n, k = 300, 40, 64
+    counts = np.random.default_rng(7).integers(0, 200, g)
+    counts[::3] = 0
+    idx, qa, sa, a, qb, sb, b = contiguous(counts.tolist(), n, k, 33)
+    d = sentinel(len(idx), n)
+    dg.dg_m_grouped_mxfp4_gemm_nt_contiguous(qa, sa, qb, sb, d, dev(idx))
+    for e in np.flatnonzero(counts):
+        rows = torch.from_numpy(np.flatnonzero(idx == e)).cuda()
+        check(d[rows], a[rows], b[e], f"expert {e}")
+    assert untouched(d[torch.from_numpy(idx < 0).cuda()])
     assert dg.dg_get_device_status() == 0
 
 
