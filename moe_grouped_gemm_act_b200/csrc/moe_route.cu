@@ -83,8 +83,8 @@ __device__ __forceinline__ float warp_sum(float v) {
 }
 
 // Experts l V .. l V + V - 1 of a row of E logits, -inf past E.  (Through L1: a lane's
-// pieces share sectors.)  `vec`: rows
-// start on a 16-byte boundary (or V elements, if that is less) and E % V == 0.
+// pieces share sectors.)  `vec`: rows start on a 16-byte boundary (or V elements, if
+// that is less) and E % V == 0.
 template <int V>
 __device__ __forceinline__ void load_row(const float *row, int E, bool vec, float x[V]) {
   const int e0 = (threadIdx.x & 31) * V;
@@ -193,7 +193,7 @@ __device__ __forceinline__ float loss_of(const RouteParams &p, float total, int 
 // together, takes the chosen one out and finds the owner's next: some twenty
 // instructions whatever V.
 enum Form { kRow, kRegisters, kWords };
-template <typename T, int V, int FORM>
+template <int V, int FORM>
 struct TopK {
   uint32_t top, best;
   uint32_t *row;  // [row_words(V)]
@@ -258,8 +258,8 @@ struct TopK {
 // tokens against 4.4 us; from V = 4 on the form above is faster: 128 experts, 8
 // choices 24.6 against 27.1 us for 32768 tokens, 1024 experts, 16 choices 28
 // against 55 us for 8192).
-template <typename T, int V>
-struct TopK<T, V, kRegisters> {
+template <int V>
+struct TopK<V, kRegisters> {
   uint32_t key[V], top, best;
   int at;  // the lane's lowest expert with key == top
   __device__ __forceinline__ void find_top() {
@@ -309,7 +309,7 @@ struct TopK<T, V, kRegisters> {
 // others negative, that is larger as unsigned numbers, so the unsigned maximum
 // is the next choice and taking it out is one subtraction per word.
 template <int V>
-struct TopK<__nv_bfloat16, V, kWords> {
+struct TopK<V, kWords> {
   uint32_t rel[V], top, best;
   __device__ __forceinline__ void find_top() {
     top = rel[0];
@@ -387,7 +387,7 @@ moe_route_kernel(const RouteParams p) {
        t += stride) {
     float x[V];
     load_row<V>(static_cast<const T *>(p.logits) + t * p.ld, E, p.vec != 0, x);
-    TopK<T, V, kForm> topk;
+    TopK<V, kForm> topk;
     topk.init(x, reinterpret_cast<uint32_t *>(s_psum + warp * kStride));
     const float xmax = topk.largest();
     // a NaN or +inf anywhere makes the sum NaN, and so does a row that is

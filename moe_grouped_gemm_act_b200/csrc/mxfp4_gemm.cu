@@ -372,55 +372,55 @@ mxfp4_gemm_kernel(const __grid_constant__ CUtensorMap tmap_a,
     // (one elected thread runs the role, and one the MMA issuer's: 0.21 us a stage
     // of a small tile; waiting with the whole warp and electing per stage, 0.24)
     if (elect_one()) {
-    Ring ring;
-    int issued = 0;  // stages, counted up to the ring's length
-    int it = 0;
-    const int starve = blockIdx.x == 0 ? p.starve : -1;
-    for_each_tile<SCHED, PAIR>(p, tab, [&](const Tile &t) {
-      const int b_block = t.group * b_blocks + t.n0 / 128;
-      const int a_block = t.slab * a_blocks + t.tok0 / 128;
-      const int a_row = t.tok0 + static_cast<int>(rank) * (mma_n<PAIR>(t) / 2);
-      for (int ks = t.k_begin; ks < t.k_end; ++ks) {
-        const int s = ring.slot;
-        if (!mbar_wait(empty_bar(s), ring.parity ^ 1, abort, p.status)) return false;
-        if (it != starve) {
-          const uint32_t sb = base + static_cast<uint32_t>(s) * stage_bytes;
-          const uint32_t sf = sf_base + static_cast<uint32_t>(s) * sf_stage;
-          const int kc = ks * (kStageK / 2), wc = ks * kStageWords;
-          if constexpr (PAIR) {
-            // both CTAs' boxes complete on rank 0's barrier
-            const uint32_t fb = mapa_shared(full_bar(s), 0);
-            if (rank == 0) mbar_arrive_expect_tx(full_bar(s), 2 * (stage_bytes + sf_stage));
-            tma_load_3d_pair(sb, &tmap_b, fb, kc, t.n0, t.group);
-            tma_load_3d_pair(sb + kBBytes, &tmap_a, fb, kc, a_row, t.slab);
-            tma_load_3d_pair(sf, &tmap_sfb, fb, 0, wc, b_block);
-            tma_load_3d_pair(sf + kSfBBytes, &tmap_sfa, fb, 0, wc, a_block);
-          } else {
-            mbar_arrive_expect_tx(full_bar(s), stage_bytes + sf_stage);
-            tma_load_3d(sb, &tmap_b, full_bar(s), kc, t.n0, t.group);
-            tma_load_3d(sb + kBBytes, &tmap_a, full_bar(s), kc, a_row, t.slab);
-            tma_load_3d(sf, &tmap_sfb, full_bar(s), 0, wc, b_block);
-            tma_load_3d(sf + kSfBBytes, &tmap_sfa, full_bar(s), 0, wc, a_block);
+      Ring ring;
+      int issued = 0;  // stages, counted up to the ring's length
+      int it = 0;
+      const int starve = blockIdx.x == 0 ? p.starve : -1;
+      for_each_tile<SCHED, PAIR>(p, tab, [&](const Tile &t) {
+        const int b_block = t.group * b_blocks + t.n0 / 128;
+        const int a_block = t.slab * a_blocks + t.tok0 / 128;
+        const int a_row = t.tok0 + static_cast<int>(rank) * (mma_n<PAIR>(t) / 2);
+        for (int ks = t.k_begin; ks < t.k_end; ++ks) {
+          const int s = ring.slot;
+          if (!mbar_wait(empty_bar(s), ring.parity ^ 1, abort, p.status)) return false;
+          if (it != starve) {
+            const uint32_t sb = base + static_cast<uint32_t>(s) * stage_bytes;
+            const uint32_t sf = sf_base + static_cast<uint32_t>(s) * sf_stage;
+            const int kc = ks * (kStageK / 2), wc = ks * kStageWords;
+            if constexpr (PAIR) {
+              // both CTAs' boxes complete on rank 0's barrier
+              const uint32_t fb = mapa_shared(full_bar(s), 0);
+              if (rank == 0) mbar_arrive_expect_tx(full_bar(s), 2 * (stage_bytes + sf_stage));
+              tma_load_3d_pair(sb, &tmap_b, fb, kc, t.n0, t.group);
+              tma_load_3d_pair(sb + kBBytes, &tmap_a, fb, kc, a_row, t.slab);
+              tma_load_3d_pair(sf, &tmap_sfb, fb, 0, wc, b_block);
+              tma_load_3d_pair(sf + kSfBBytes, &tmap_sfa, fb, 0, wc, a_block);
+            } else {
+              mbar_arrive_expect_tx(full_bar(s), stage_bytes + sf_stage);
+              tma_load_3d(sb, &tmap_b, full_bar(s), kc, t.n0, t.group);
+              tma_load_3d(sb + kBBytes, &tmap_a, full_bar(s), kc, a_row, t.slab);
+              tma_load_3d(sf, &tmap_sfb, full_bar(s), 0, wc, b_block);
+              tma_load_3d(sf + kSfBBytes, &tmap_sfa, full_bar(s), 0, wc, a_block);
+            }
           }
+          ring.advance(p.stages);
+          if (issued < p.stages) ++issued;
+          ++it;
         }
-        ring.advance(p.stages);
-        if (issued < p.stages) ++issued;
-        ++it;
-      }
-      return true;
-    });
-    // no copy may still be writing this CTA's shared memory when it exits: wait
-    // for the last use of every stage that was armed (pair: rank 0's barriers
-    // count both CTAs' bytes, and rank 1 leaves after rank 0 at the cluster
-    // barrier)
-    volatile int never = 0;
-    if (rank == 0)
-      for (int i = 0; i < issued; ++i) {
-        // slots before the ring's place were used with its parity, the others
-        // with the one before (a stage that was left out has no copies)
-        if (starve < 0 || it <= starve || i != starve % p.stages)
-          mbar_wait(full_bar(i), i < ring.slot ? ring.parity : ring.parity ^ 1, &never, p.status);
-      }
+        return true;
+      });
+      // no copy may still be writing this CTA's shared memory when it exits: wait
+      // for the last use of every stage that was armed (pair: rank 0's barriers
+      // count both CTAs' bytes, and rank 1 leaves after rank 0 at the cluster
+      // barrier)
+      volatile int never = 0;
+      if (rank == 0)
+        for (int i = 0; i < issued; ++i) {
+          // slots before the ring's place were used with its parity, the others
+          // with the one before (a stage that was left out has no copies)
+          if (starve < 0 || it <= starve || i != starve % p.stages)
+            mbar_wait(full_bar(i), i < ring.slot ? ring.parity : ring.parity ^ 1, &never, p.status);
+        }
     }
     __syncwarp();
   } else if (warp == 1) {
@@ -443,51 +443,49 @@ mxfp4_gemm_kernel(const __grid_constant__ CUtensorMap tmap_a,
           const int s = ring.slot;
           if (!mbar_wait(full_bar(s), ring.parity, abort, p.status)) return false;
           tc_fence_after();
-          {
-            // (descriptor addresses are in units of 16 bytes, below 2^14: no carry)
-            const uint64_t bdesc = bdesc0 + static_cast<uint32_t>(s) * (stage_bytes >> 4);
-            const uint64_t adesc = bdesc + (kBBytes >> 4);
-            const uint64_t sfdesc = sfdesc0 + static_cast<uint32_t>(s) * (sf_stage >> 4);
-            const uint32_t slot = tmem + sf_col + (it % kSfSlots) * kSfSlotCols;
-            const uint32_t first = ks == t.k_begin ? 1u : 0u;
-            auto cp = [&](uint32_t to, uint32_t from) {
-              if constexpr (PAIR) tmem_cp_32x128b_x4_pair(slot + to, sfdesc + (from >> 4));
-              else tmem_cp_32x128b_x4(slot + to, sfdesc + (from >> 4));
-            };
-            auto scales = [&](int w) {
-              cp(4 * w, kMxBlockBytes * w);
-              cp(8 + 8 * w, kSfBBytes + kMxBlockBytes * w);
-              if (second) cp(12 + 8 * w, 2 * kSfBBytes + kMxBlockBytes * w);
-            };
-            auto mma = [&](int j) {
-              const uint32_t sfb = slot + 4 * (j >> 1), sfa = slot + 8 + 8 * (j >> 1);
-              const uint32_t more = j > 0 ? 1u : first ^ 1u;
-              if constexpr (PAIR)
-                umma_mxf4_pair(d, bdesc + 2 * j, adesc + 2 * j, idesc, sfb, sfa, 2u * (j & 1),
-                               more);
-              else
-                umma_mxf4(d, bdesc + 2 * j, adesc + 2 * j, idesc, sfb, sfa, 2u * (j & 1), more);
-            };
-            const int mmas = k_mmas - ks * (kStageK / kMmaK);
-            scales(0);
-            if (mmas >= kStageK / kMmaK) {
-              scales(1);
+          // (descriptor addresses are in units of 16 bytes, below 2^14: no carry)
+          const uint64_t bdesc = bdesc0 + static_cast<uint32_t>(s) * (stage_bytes >> 4);
+          const uint64_t adesc = bdesc + (kBBytes >> 4);
+          const uint64_t sfdesc = sfdesc0 + static_cast<uint32_t>(s) * (sf_stage >> 4);
+          const uint32_t slot = tmem + sf_col + (it % kSfSlots) * kSfSlotCols;
+          const uint32_t first = ks == t.k_begin ? 1u : 0u;
+          auto cp = [&](uint32_t to, uint32_t from) {
+            if constexpr (PAIR) tmem_cp_32x128b_x4_pair(slot + to, sfdesc + (from >> 4));
+            else tmem_cp_32x128b_x4(slot + to, sfdesc + (from >> 4));
+          };
+          auto scales = [&](int w) {
+            cp(4 * w, kMxBlockBytes * w);
+            cp(8 + 8 * w, kSfBBytes + kMxBlockBytes * w);
+            if (second) cp(12 + 8 * w, 2 * kSfBBytes + kMxBlockBytes * w);
+          };
+          auto mma = [&](int j) {
+            const uint32_t sfb = slot + 4 * (j >> 1), sfa = slot + 8 + 8 * (j >> 1);
+            const uint32_t more = j > 0 ? 1u : first ^ 1u;
+            if constexpr (PAIR)
+              umma_mxf4_pair(d, bdesc + 2 * j, adesc + 2 * j, idesc, sfb, sfa, 2u * (j & 1),
+                             more);
+            else
+              umma_mxf4(d, bdesc + 2 * j, adesc + 2 * j, idesc, sfb, sfa, 2u * (j & 1), more);
+          };
+          const int mmas = k_mmas - ks * (kStageK / kMmaK);
+          scales(0);
+          if (mmas >= kStageK / kMmaK) {
+            scales(1);
 #pragma unroll
-              for (int j = 0; j < kStageK / kMmaK; ++j) mma(j);
-            } else {
-              // the last stage of a K off the 256 grid
-              if (mmas > 2) scales(1);
-              mma(0);
-              if (mmas > 1) mma(1);
-              if (mmas > 2) mma(2);
-            }
-            if constexpr (PAIR) {
-              umma_commit_pair_both(empty_bar(s));
-              if (ks + 1 == t.k_end) umma_commit_pair_both(tfull_bar(buf));
-            } else {
-              umma_commit(empty_bar(s));
-              if (ks + 1 == t.k_end) umma_commit(tfull_bar(buf));
-            }
+            for (int j = 0; j < kStageK / kMmaK; ++j) mma(j);
+          } else {
+            // the last stage of a K off the 256 grid
+            if (mmas > 2) scales(1);
+            mma(0);
+            if (mmas > 1) mma(1);
+            if (mmas > 2) mma(2);
+          }
+          if constexpr (PAIR) {
+            umma_commit_pair_both(empty_bar(s));
+            if (ks + 1 == t.k_end) umma_commit_pair_both(tfull_bar(buf));
+          } else {
+            umma_commit(empty_bar(s));
+            if (ks + 1 == t.k_end) umma_commit(tfull_bar(buf));
           }
           ring.advance(p.stages);
         }
@@ -495,10 +493,8 @@ mxfp4_gemm_kernel(const __grid_constant__ CUtensorMap tmap_a,
         return true;
       });
       // every MMA issued above completes before TMEM is freed
-      {
-        if constexpr (PAIR) umma_commit_pair_own(drain_bar);
-        else umma_commit(drain_bar);
-      }
+      if constexpr (PAIR) umma_commit_pair_own(drain_bar);
+      else umma_commit(drain_bar);
       volatile int never = 0;
       mbar_wait(drain_bar, 0, &never, p.status);
     }

@@ -345,8 +345,7 @@ __device__ __forceinline__ void decode_store<__nv_bfloat16>(__nv_bfloat16 *p,
   }
 }
 
-constexpr int kReadPass = 32 * 16;  // elements a warp reads back per pass
-constexpr int kReadPasses = 1;
+constexpr int kReadPass = 32 * 16;  // elements a warp reads back
 
 template <typename T>
 __global__ void __launch_bounds__(kThreads)
@@ -356,33 +355,18 @@ dequantize_mxfp4_kernel(const uint8_t *__restrict__ q, const uint32_t *__restric
   grid_dependency_wait();
   const int lane = threadIdx.x & 31;
   const int words = (K + 127) / 128, blocks = (M + 127) / 128;
-  const int k0 = blockIdx.x * (kReadPass * kReadPasses) + lane * 16;
+  const int k = blockIdx.x * kReadPass + lane * 16;
   for (int b = blockIdx.z; b < batch; b += gridDim.z) {
     for (int r = blockIdx.y * (kThreads / 32) + (threadIdx.x >> 5); r < M;
          r += gridDim.y * (kThreads / 32)) {
       const int64_t row = static_cast<int64_t>(b) * M + r;
-      const uint8_t *qrow = q + row * (K / 2) + k0 / 2;
       const uint32_t *srow = sf + (static_cast<int64_t>(b) * blocks + (r >> 7)) * words *
                                       kMxBlockWords + (r & 31) * 4 + ((r & 127) >> 5);
-      uint2 code[kReadPasses];
-      uint32_t word[kReadPasses];
-#pragma unroll
-      for (int i = 0; i < kReadPasses; ++i) {
-        const int k = k0 + i * kReadPass;
-        code[i] = make_uint2(0, 0);
-        word[i] = 0;
-        if (k < K) {
-          code[i] = __ldcs(reinterpret_cast<const uint2 *>(qrow + i * (kReadPass / 2)));
-          word[i] = __ldcg(srow + static_cast<int64_t>(k / 128) * kMxBlockWords);
-        }
-      }
-#pragma unroll
-      for (int i = 0; i < kReadPasses; ++i) {
-        const int k = k0 + i * kReadPass;
-        if (k < K) {
-          const uint32_t c[2] = {code[i].x, code[i].y};
-          decode_store<T>(y + row * ld_y + k, c, (word[i] >> (8 * ((lane >> 1) & 3))) & 255u);
-        }
+      if (k < K) {
+        const uint2 code = __ldcs(reinterpret_cast<const uint2 *>(q + row * (K / 2) + k / 2));
+        const uint32_t word = __ldcg(srow + static_cast<int64_t>(k / 128) * kMxBlockWords);
+        const uint32_t c[2] = {code.x, code.y};
+        decode_store<T>(y + row * ld_y + k, c, (word >> (8 * ((lane >> 1) & 3))) & 255u);
       }
     }
   }
@@ -489,7 +473,7 @@ extern "C" int dg_dequantize_mxfp4(const uint8_t *q, const int32_t *sf, int64_t 
   if (rc) return rc;
   cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
   const uint32_t *w = reinterpret_cast<const uint32_t *>(sf);
-  const dim3 grid = row_grid(K, kReadPass * kReadPasses, M, batch);
+  const dim3 grid = row_grid(K, kReadPass, M, batch);
   const int b = static_cast<int>(batch), m = static_cast<int>(M), k = static_cast<int>(K);
   if (y_dtype == DG_DTYPE_F32)
     return launch(dequantize_mxfp4_kernel<float>, grid, s, q, w, b, m, k,
