@@ -669,7 +669,8 @@ size_t dg_moe_route_workspace_size(int64_t T, int E);
  *   dlogits[t][e] = p[e] (c[e] - <p, c>)
  *       + (normalize) w_j (dw_j - <w, dw>) where e = idx[t][j]
  *       + (else)      w_j dw_j where e = idx[t][j], - p[e] <w, dw>
- * Zero for tokens that did not route, for closed experts, and for the
+ * Zero for tokens that did not route, whatever their logits and dweights hold,
+ * for closed experts (where dweights and dloss are finite), and for the
  * gradients of choices that are -1.
  *
  *   idx, weights, counts, num_tokens  as dg_moe_route wrote them.

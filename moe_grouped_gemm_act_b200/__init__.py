@@ -741,7 +741,8 @@ def _mx_scales(rows, k):
 def dg_quantize_mxfp4(x: torch.Tensor, transpose: bool = False, q=None, sf=None, stream=None):
     """MXFP4 quantization (one UE8M0 scale per 32 K elements) of x [M, K] or
     [B, M, K] (float32 or bfloat16), or, with ``transpose``, of the transpose of
-    x [K, M].  A 2-D x may have any row stride.
+    x [K, M].  A 2-D x may have a row stride: with ``transpose`` any, else one of a
+    multiple of 16 bytes (and a base on 16 bytes), or DG_ERR_ALIGNMENT is raised.
 
     Returns (q uint8 [.., M, K/2], sf int32 [.., ceil(M/128), ceil(K/128), 32, 4]),
     the layouts of include/dg.h."""
@@ -886,7 +887,9 @@ def dg_moe_route(logits: torch.Tensor, top_k: int, normalize: bool = True, token
 
     Returns (idx int32 [T, top_k], weights float32 [T, top_k], counts int32 [E],
     loss float32 [1], num_tokens int32 [1]); -1 / 0 where a token has no choice.
-    The five are views of one allocation."""
+    The five are views of one allocation: each keeps all of it alive (copy a loss that
+    is kept for a log).  They carry no autograd graph; the gradient is
+    dg_moe_route_backward's."""
     t, e, ld = _route_logits(logits)
     dev = logits.device
     if token_mask is not None:

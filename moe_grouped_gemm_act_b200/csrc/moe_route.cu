@@ -43,16 +43,20 @@ constexpr int kMaxExperts = 1024;
 constexpr int kMaxTopK = 32;  // lane j keeps choice j
 constexpr int kFinishCtas = 8;  // one cluster
 // Up to this many tokens (two per warp of it) one cluster does everything in one
-// launch; above it a second kernel joins the blocks' sums (256 experts, BF16: 256
-// tokens 6.3 against 6.1 us and one launch and one workspace less on the host, 512
-// tokens 10.1 against 6.3 us).
+// launch; above it a second kernel joins the blocks' sums.  One cluster against the
+// join, on the GPU: 32 experts, FP32, 128 / 256 / 512 tokens 3.8 / 5.3 / 8.0 against
+// 4.9 / 5.2 / 5.2 us; 256 experts, BF16, 4.5 / 6.4 / 10.1 against 5.9 / 6.0 / 6.4 us;
+// 1024 experts, FP32, 11.7 / 16.7 / 25.6 against 13.6 / 13.7 / 13.9 us.  So at 256
+// tokens it loses up to 3 us there, and saves a launch and a workspace on the host.
 constexpr int kClusterTokens = 2 * kWarps * kFinishCtas;
 
 // Resident blocks per SM that an instance with V experts per lane is compiled
 // for: a token is a chain of shuffles and warp maxima whose latency other warps
-// hide, but fewer registers than these leave spill (V = 8 with three blocks:
-// 26.8 us against 24.2 us for 32768 tokens of 256 experts; V = 2 with two: 27.9
-// against 17.7 us for 64 experts).
+// hide, but with fewer registers than these leave it spills (V = 8 with three
+// blocks: 26.8 us against 24.2 us for 32768 tokens of 256 experts; V = 2 with two:
+// 27.9 against 17.7 us for 64 experts).  The one-cluster instances take the same
+// figure, and with V = 1 and 2 spill 68 to 196 bytes; BF16 with V = 32 spills 12 to
+// 16 bytes in both forms.
 constexpr int resident(int v) { return v <= 2 ? 4 : v == 4 ? 3 : v == 8 ? 2 : 1; }
 
 // Order-preserving key of an FP32 value that is not NaN; -0 and +0 are one key.
@@ -184,8 +188,10 @@ __device__ __forceinline__ float loss_of(const RouteParams &p, float total, int 
 // first is the row's largest, which the softmax has found, and the last is not
 // taken out (one round less of k: 32768 tokens of 256 experts, BF16, 24.8 -> 24.2
 // us).
-// (The kernel is bound by the ALU pipe -- compares, selects and integer maxima
-// -- so a round has few of them per expert.)
+// (Compares, selects and integer maxima keep the ALU pipe at 57 %, so a round has
+// few of them per expert: 32768 tokens of 256 experts take 19.0 us at k = 1 and 25.2
+// at k = 8 in BF16, 18.9 and 28.3 in FP32.  The larger part of the time is what a
+// token costs whatever k: its exponentials, divisions, warp sums and keys.)
 //
 // kRow: a lane keeps its largest key, the others wait in the warp's
 // row of shared memory.  A round is a warp maximum; the lowest lane that holds
@@ -405,6 +411,8 @@ moe_route_kernel(const RouteParams p) {
     float my_w = 0.0f;
     if (!masked && sum == sum) {
       ++routed;
+      // (a product with the reciprocal: one FP32 rounding more than a division for
+      // each expert)
       const float inv = 1.0f / sum;
 #pragma unroll
       for (int i = 0; i < V; ++i) psum[i] += x[i] * inv;
@@ -568,7 +576,11 @@ moe_route_finish_kernel(const RouteParams p, int blocks) {
 }
 
 // The gradient of the logits.  A token that did not route (idx[t][0] < 0) gets
-// zeros; its logits are not used, so what they hold does not matter.
+// zeros; its logits are not used, so what they hold does not matter.  Probabilities
+// are products with the reciprocal of their sum, as in the forward kernel.  A warp
+// takes its tokens one after another and asks for a token's logits once its choices
+// are there: two round trips each bound it (32768 tokens of 256 experts, BF16: ALU
+// pipe 26 %, DRAM 12 %; 16 us, FP32 17 us).
 struct RouteBackwardParams {
   const void *logits;
   int64_t tokens, ld;

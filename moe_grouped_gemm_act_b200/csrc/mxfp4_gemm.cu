@@ -884,6 +884,12 @@ int launch_forms(const Operands &o, MxParams p, cudaStream_t stream) {
     if constexpr (SCHED == kMxContiguous) {
       const int most = p.rows / 128;  // blocks that may hold an expert's rows
       const int n_pairs = ceil_div(p.n, 2 * kTileN);
+      // Pairs for two tiles or more each, counted as if no run of an expert's blocks had
+      // an odd length.  13 experts of 1448 x 1056: 42 to 72 tiles 10.1 to 11.9 us single
+      // against 11.5 to 13.6, 156 tiles 19.9 against 17.5; 32 of 2048 x 1024: 128 tiles
+      // 11.6 against 12.2, 184 tiles 15.2 against 16.9, 240 tiles 18.5 against 18.3; 8 of
+      // 4096 x 7168: 64 tiles 25.9 against 26.3, 112 tiles 40.6 against 30.9, 528 tiles
+      // 159 against 103.
       if (pairs > 0 && ceil_div(most, 2) * n_pairs >= 2 * pairs) {
         p.tok_tile = 256;
         p.n_tiles = n_pairs;
@@ -899,6 +905,12 @@ int launch_forms(const Operands &o, MxParams p, cudaStream_t stream) {
       if (half_sms(p.tok_tile, tiles, sms, info->num_sms))
         return launch_form<SCHED, false, true>(o, p, tiles < 2 * sms ? tiles : 2 * sms, max,
                                                stream);
+      // Pairs where there is a tile of 256 x 256 for each: 768 x 7168 x 7168, 84 of
+      // them for 74 pairs, 21.6 us against 25.4 with single CTAs, 2048 x 7168 x 7168 39.8
+      // against 45.8.  With fewer, single CTAs (K split where there are SMs for it) are
+      // as often the faster: 2112 x 7168, 9 / 18 / 36 tiles, 14.3 / 12.5 / 13.6 us against
+      // 17.4 / 14.3 / 13.9 with pairs; 4096 x 2048, 16 / 32 / 64 tiles, 9.9 / 10.2 / 8.1
+      // against 8.0 / 8.4 / 9.3; 512 x 7168 x 7168, 56 tiles, 16.4 against 15.4.
       const int pair_tiles = p.tok_tiles * ceil_div(p.n, 2 * kTileN);
       if (p.tok_tile == 256 && pairs > 0 && pair_tiles >= pairs) {
         p.n_tiles = ceil_div(p.n, 2 * kTileN);
