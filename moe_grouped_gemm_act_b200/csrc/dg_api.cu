@@ -33,15 +33,13 @@ const DeviceInfo *device_info() {
   if (cudaGetDevice(&dev) != cudaSuccess || dev < 0 || dev >= kMaxDevices) return nullptr;
   std::call_once(g_info_once[dev], [dev] {
     DeviceInfo &d = g_info[dev];
-    int major = 0, sms = 0, smem = 0, per_sm = 0;
+    int major = 0, sms = 0, smem = 0;
     cudaDeviceGetAttribute(&major, cudaDevAttrComputeCapabilityMajor, dev);
     cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev);
     cudaDeviceGetAttribute(&smem, cudaDevAttrMaxSharedMemoryPerBlockOptin, dev);
-    cudaDeviceGetAttribute(&per_sm, cudaDevAttrMaxSharedMemoryPerMultiprocessor, dev);
     d.ok = (major == 10) ? 1 : 0;
     d.num_sms = sms;
     d.max_smem_optin = smem;
-    d.smem_per_sm = per_sm;
     // resolve the status word's device address (this also loads the module,
     // so later calls can be captured into a CUDA graph)
     void *st = nullptr;

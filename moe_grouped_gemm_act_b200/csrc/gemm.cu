@@ -1979,12 +1979,29 @@ size_t gemm_workspace_size(int64_t M, int64_t N, int64_t K, int num_sms) {
   return need == 0 ? 0 : (need + 255) & ~static_cast<size_t>(255);
 }
 
-TestKnobs test_knobs() {
+// Test knobs of the abort path (both unset in normal use):
+// DG_TEST_STARVE_LOAD=i makes CTA 0's producer leave out the loads of its
+// iteration i (a kernel parameter); DG_TEST_WAIT_LIMIT_US=t lowers every
+// wait's limit to t microseconds (at least kWaitCheckNs), written to the
+// device before this call's kernel and put back after it, in stream order.
+struct TestKnobs {
+  int starve = -1;
+  unsigned long long limit_ns = kWaitLimitNs;
+};
+
+static TestKnobs test_knobs() {
   TestKnobs k;
   if (const char *e = getenv("DG_TEST_STARVE_LOAD")) k.starve = atoi(e);
   if (const char *e = getenv("DG_TEST_WAIT_LIMIT_US"))
     k.limit_ns = strtoull(e, nullptr, 10) * 1000ull;
   return k;
+}
+
+static int set_wait_limit(unsigned long long limit_ns, cudaStream_t stream) {
+  return cudaMemcpyToSymbolAsync(g_wait_limit_ns, &limit_ns, sizeof(limit_ns), 0,
+                                 cudaMemcpyHostToDevice, stream) == cudaSuccess
+             ? DG_OK
+             : DG_ERR_CUDA;
 }
 
 static int launch_fp8_gemm_impl(int sched, const uint8_t *A, const uint8_t *B, GemmParams p,
@@ -1995,12 +2012,12 @@ int launch_fp8_gemm(int sched, const uint8_t *A, const uint8_t *B, GemmParams p,
                     cudaStream_t stream, int num_sms, size_t ws_bytes, void *ws, int layout) {
   const TestKnobs knobs = test_knobs();
   p.starve_it = knobs.starve;
-  if (knobs.limit_ns == 0)
+  if (knobs.limit_ns == kWaitLimitNs)
     return launch_fp8_gemm_impl(sched, A, B, p, stream, num_sms, ws_bytes, ws, layout);
-  int rc = cuda_status(set_wait_limit(knobs.limit_ns, stream));
+  int rc = set_wait_limit(knobs.limit_ns, stream);
   if (rc) return rc;
   rc = launch_fp8_gemm_impl(sched, A, B, p, stream, num_sms, ws_bytes, ws, layout);
-  const int rc2 = cuda_status(set_wait_limit(kWaitLimitNs, stream));
+  const int rc2 = set_wait_limit(kWaitLimitNs, stream);
   return rc ? rc : rc2;
 }
 

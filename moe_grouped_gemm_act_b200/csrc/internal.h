@@ -33,14 +33,6 @@ inline cudaLaunchAttribute pdl_attribute() {
   return a;
 }
 
-// A CUDA call's outcome as a status.  A failure is taken out of the runtime's
-// last-error slot: the next entry point that asks for it would report it as its own.
-inline int cuda_status(cudaError_t e) {
-  if (e == cudaSuccess) return DG_OK;
-  (void)cudaGetLastError();
-  return DG_ERR_CUDA;
-}
-
 // ---------------------------------------------------------------- GEMM
 // kDenseCluster: dense tiles every one split `splits` ways along K, the splits
 // of a tile forming one thread-block cluster that reduces through
@@ -155,25 +147,12 @@ int launch_fp8_gemm(int sched, const uint8_t *A, const uint8_t *B,
 
 size_t gemm_workspace_size(int64_t M, int64_t N, int64_t K, int num_sms);
 
-// ---------------------------------------------------------------- test knobs
-// Of the abort path, both unset in normal use: DG_TEST_STARVE_LOAD=i makes CTA 0's
-// producer leave out the loads of its iteration i (a kernel parameter, -1: none);
-// DG_TEST_WAIT_LIMIT_US=t lowers every wait's limit to t microseconds (at least
-// kWaitCheckNs), written to the device before the call's kernel and put back after
-// it, in stream order.
-struct TestKnobs {
-  int starve = -1;
-  unsigned long long limit_ns = 0;  // 0: the limit as it is
-};
-TestKnobs test_knobs();
-
 // ---------------------------------------------------------------- device state
 struct DeviceInfo {
-  int ok;              // 1 when the device is usable (sm_100)
+  int ok;            // 1 when the device is usable (sm_100)
   int num_sms;
-  int max_smem_optin;  // shared memory a block may ask for
-  int smem_per_sm;     // what an SM has for all its blocks
-  int *status;         // device address of the status word
+  int max_smem_optin;
+  int *status;       // device address of the status word
 };
 
 // Per-device properties (cached); returns nullptr on a CUDA error.

@@ -30,6 +30,7 @@
 #include <cstdint>
 
 #include "dg.h"
+#include "host.h"
 #include "internal.h"
 #include "ptx.cuh"
 

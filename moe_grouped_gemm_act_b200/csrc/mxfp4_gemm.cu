@@ -17,8 +17,10 @@
 
 #include <atomic>
 #include <cstdint>
+#include <cstdlib>
 
 #include "dg.h"
+#include "host.h"
 #include "internal.h"
 #include "mxfp4.cuh"
 #include "ptx.cuh"
@@ -699,9 +701,19 @@ constexpr int kMaxDevices = 64;
 // shared memory, eight bytes a block); more rows are several launches.
 constexpr int kMaxContiguousRows = 2048 * 128;
 
+// Shared memory that an SM has for all its CTAs; 0 on a CUDA error.
+int smem_per_sm(int dev) {
+  static std::atomic<int> known[kMaxDevices];  // (any thread may be the first)
+  int v = known[dev].load(std::memory_order_relaxed);
+  if (v == 0 && cuda_status(cudaDeviceGetAttribute(
+                    &v, cudaDevAttrMaxSharedMemoryPerMultiprocessor, dev)) == DG_OK)
+    known[dev].store(v, std::memory_order_relaxed);
+  return v;
+}
+
 template <int SCHED, bool PAIR, bool HALF>
 int configure(int dev, int smem) {
-  static std::atomic<bool> done[kMaxDevices];  // (any thread may be the first)
+  static std::atomic<bool> done[kMaxDevices];
   if (done[dev].load(std::memory_order_relaxed)) return DG_OK;
   const int rc = cuda_status(cudaFuncSetAttribute(
       mxfp4_gemm_kernel<SCHED, PAIR, HALF>, cudaFuncAttributeMaxDynamicSharedMemorySize, smem));
@@ -855,7 +867,9 @@ int launch_forms(const Operands &o, MxParams p, cudaStream_t stream) {
   if (!info || cudaGetDevice(&dev) != cudaSuccess || dev < 0 || dev >= kMaxDevices)
     return DG_ERR_CUDA;
   const int sms = effective_num_sms();
-  const Smem max = smem_limits(info->max_smem_optin, info->smem_per_sm);
+  const int per_sm = smem_per_sm(dev);
+  if (per_sm <= 0) return DG_ERR_CUDA;
+  const Smem max = smem_limits(info->max_smem_optin, per_sm);
   int rc = configure<SCHED, false, false>(dev, max.full);
   if (!rc && SCHED != kMxContiguous)
     rc = configure<SCHED, false, SCHED != kMxContiguous>(dev, max.half);
@@ -925,15 +939,24 @@ int launch_forms(const Operands &o, MxParams p, cudaStream_t stream) {
   }
 }
 
+// The limit of this file's bounded waits, from here on in stream order.
+int set_wait_limit(unsigned long long limit_ns, cudaStream_t stream) {
+  return cuda_status(cudaMemcpyToSymbolAsync(g_wait_limit_ns, &limit_ns, sizeof(limit_ns), 0,
+                                             cudaMemcpyHostToDevice, stream));
+}
+
+// With the abort path's test knobs (gemm.cu's, both unset in normal use):
+// DG_TEST_STARVE_LOAD=i makes CTA 0's producer leave out the loads of its i-th stage,
+// DG_TEST_WAIT_LIMIT_US=t lowers the waits' limit to t microseconds for this call.
 template <int SCHED>
 int launch_mxfp4(const Operands &o, MxParams p, cudaStream_t stream) {
-  const TestKnobs knobs = test_knobs();
-  p.starve = knobs.starve;
-  if (knobs.limit_ns == 0) return launch_forms<SCHED>(o, p, stream);
-  int rc = cuda_status(set_wait_limit(knobs.limit_ns, stream));
+  const char *starve = getenv("DG_TEST_STARVE_LOAD"), *limit = getenv("DG_TEST_WAIT_LIMIT_US");
+  p.starve = starve ? atoi(starve) : -1;
+  if (!limit) return launch_forms<SCHED>(o, p, stream);
+  int rc = set_wait_limit(strtoull(limit, nullptr, 10) * 1000ull, stream);
   if (rc) return rc;
   rc = launch_forms<SCHED>(o, p, stream);
-  const int rc2 = cuda_status(set_wait_limit(kWaitLimitNs, stream));
+  const int rc2 = set_wait_limit(kWaitLimitNs, stream);
   return rc ? rc : rc2;
 }
 

@@ -11,6 +11,7 @@
 #include <cstdint>
 
 #include "dg.h"
+#include "host.h"
 #include "internal.h"
 #include "mxfp4.cuh"
 #include "ptx.cuh"

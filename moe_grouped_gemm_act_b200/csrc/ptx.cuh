@@ -7,8 +7,6 @@
 // false so that the caller can leave its loop and let the CTA exit cleanly.
 #pragma once
 
-#include <cuda_runtime.h>
-
 #include <cstdint>
 
 #include "dg.h"
@@ -27,10 +25,6 @@ constexpr uint64_t kWaitLimitNs = 2000000000ull;
 // applies (one copy per translation unit).  Its host side may lower it for a
 // test that starves a wait on purpose, so that the wait runs out quickly.
 static __device__ unsigned long long g_wait_limit_ns = kWaitLimitNs;
-static inline cudaError_t set_wait_limit(unsigned long long limit_ns, cudaStream_t stream) {
-  return cudaMemcpyToSymbolAsync(g_wait_limit_ns, &limit_ns, sizeof(limit_ns), 0,
-                                 cudaMemcpyHostToDevice, stream);
-}
 
 // Waits shorter than this never read g_wait_limit_ns, so that the limit's
 // global load (cold in every cache at a kernel's start) stays off the path of
